@@ -18,7 +18,9 @@ BBS_OK, BBS_EINVAL, BBS_ENOTSUP, BBS_EHIP = 0, -1, -2, -3
 RTN, SR = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 FMT_NVFP4, FMT_MXFP8, FMT_MXFP4 = 0, 1, 2
+ACT_SILU, ACT_GELU = 0, 1
 AMAX_WS_FLOATS = 11264
+GEMV_MAX_TOKENS = 64
 
 
 class Fp4Desc(C.Structure):
@@ -88,7 +90,14 @@ def _load():
     lib.s2f6_quantize.argtypes = [vp, i64, i64, i64, i32, C.c_uint32, C.POINTER(S2F6Desc), vp]
     lib.s2f6_combine.argtypes = [C.POINTER(S2F6Desc), vp, vp, i64, i32, i32, C.c_uint32, vp, i32,
                                  i64, vp]
-    for f in ("nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_requantize_t", "nvfp4_gemm", "grouped_nvfp4_gemm",
+    lib.nvfp4_gated_gemm.argtypes = [C.POINTER(Fp4Desc), C.POINTER(Fp4Desc), C.POINTER(Fp4Desc), i32,
+                                     vp, i32, i64, C.POINTER(Mx8Desc), C.POINTER(Mx8Desc), vp]
+    lib.mxfp8_gemm_gated_bwd.argtypes = [C.POINTER(Mx8Desc), C.POINTER(Mx8Desc), C.POINTER(Mx8Desc),
+                                         C.POINTER(Mx8Desc), i32, vp, vp, i32, i64, vp]
+    lib.nvfp4_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i64, vp]
+    lib.nvfp4_gated_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, vp, i32, i64, vp]
+    for f in ("nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
+              "nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_requantize_t", "nvfp4_gemm", "grouped_nvfp4_gemm",
               "s2f6_quantize", "s2f6_combine", "mxfp4_quantize", "nvfp4_gemm_quant",
               "grouped_nvfp4_gemm_quant", "nvfp4_gemm_s2f6", "grouped_nvfp4_gemm_s2f6"):
         getattr(lib, f).restype = C.c_int
@@ -323,3 +332,49 @@ def grouped_nvfp4_gemm_s2f6(A, row_index, group_offsets, G, max_rows, B, N, Y, r
     _check(lib.grouped_nvfp4_gemm_s2f6(C.byref(ad), _ptr(row_index), _ptr(group_offsets), G,
                                        max_rows, C.byref(bd), N, int(rht), signs, C.byref(yd),
                                        _stream(stream)))
+
+
+def nvfp4_gated_gemm(A, Wg, Wu, H, h_dtype, act=ACT_SILU, g_ckpt=None, u_ckpt=None, ldh=None,
+                     stream=None):
+    """H = act(A * Wg^T) * (A * Wu^T) in one kernel (NVFP4Tensors A [M, K], Wg and
+    Wu [F, K]); g_ckpt and u_ckpt (MXFP8Tensors [M, F], both or neither) receive
+    8-bit checkpoints of the two products for mxfp8_gemm_gated_bwd."""
+    ad, gd, ud = A.desc(), Wg.desc(), Wu.desc()
+    g8 = g_ckpt.desc() if g_ckpt is not None else None
+    u8 = u_ckpt.desc() if u_ckpt is not None else None
+    ldh = H.stride(0) if ldh is None else ldh
+    _check(lib.nvfp4_gated_gemm(C.byref(ad), C.byref(gd), C.byref(ud), act, _ptr(H), h_dtype, ldh,
+                                C.byref(g8) if g8 is not None else None,
+                                C.byref(u8) if u8 is not None else None, _stream(stream)))
+
+
+def mxfp8_gemm_gated_bwd(dY, Wt, g_ckpt, u_ckpt, dG, dU, dtype, act=ACT_SILU, ld=None, stream=None):
+    """Backward pass of act(g) * u behind a down projection, from the 8-bit
+    checkpoints: with dH = dY * Wt^T (MXFP8Tensors [M, K], [F, K]), dG = dH * u *
+    act'(g) and dU = dH * act(g), both [M, F] with one row stride (they may be
+    the halves of one [M, 2F] tensor)."""
+    if ld is None:
+        ld = dG.stride(0)
+        if dU.stride(0) != ld:
+            raise ValueError("dG and dU must have the same row stride")
+    yd, wd, gd, ud = dY.desc(), Wt.desc(), g_ckpt.desc(), u_ckpt.desc()
+    _check(lib.mxfp8_gemm_gated_bwd(C.byref(yd), C.byref(wd), C.byref(gd), C.byref(ud), act, _ptr(dG),
+                                    _ptr(dU), dtype, ld, _stream(stream)))
+
+
+def nvfp4_gemv(fmt, x, W, y, y_dtype, ldy=None, stream=None):
+    """y = x * W^T for 1 to GEMV_MAX_TOKENS tokens: x BF16 patterns [T, K] (row
+    stride x.stride(0)), W an NVFP4Tensor or MXFP4Tensor [N, K] by fmt."""
+    wd = W.desc()
+    ldy = y.stride(0) if ldy is None else ldy
+    _check(lib.nvfp4_gemv(fmt, _ptr(x), x.shape[0], x.stride(0), C.byref(wd), _ptr(y), y_dtype, ldy,
+                          _stream(stream)))
+
+
+def nvfp4_gated_gemv(fmt, x, Wg, Wu, h, h_dtype, act=ACT_SILU, ldh=None, stream=None):
+    """h = act(x * Wg^T) * (x * Wu^T) for 1 to GEMV_MAX_TOKENS tokens, operands as
+    nvfp4_gemv."""
+    gd, ud = Wg.desc(), Wu.desc()
+    ldh = h.stride(0) if ldh is None else ldh
+    _check(lib.nvfp4_gated_gemv(fmt, _ptr(x), x.shape[0], x.stride(0), C.byref(gd), C.byref(ud), act,
+                                _ptr(h), h_dtype, ldh, _stream(stream)))

@@ -9,7 +9,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbbs.so")
 SOURCES = ["abi.hip", "quantize.hip", "gemm.hip", "gemm_nvfp4.hip", "gemm_mxfp8.hip",
-           "codec.hip"]
+           "codec.hip", "gated.hip", "gemv.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

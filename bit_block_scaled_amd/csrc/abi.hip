@@ -9,6 +9,7 @@
 
 #include "../../include/bbs.h"
 #include "bbs_kernels.hpp"
+#include "gated.hpp"
 
 static_assert(bbs::kWorkspaceFloats == BBS_AMAX_WS_FLOATS, "workspace size mismatch");
 
@@ -662,6 +663,172 @@ int grouped_nvfp4_gemm(const bbs_fp4 *A, const int32_t *row_index, const int64_t
     return hip_status(bbs::launch_grouped_nvfp4_gemm(p, c_dtype == BBS_OUT_BF16,
                                                      reinterpret_cast<hipStream_t>(stream)),
                       "grouped gemm launch");
+}
+
+namespace {
+
+bool act_ok(int32_t act) { return act == BBS_ACT_SILU || act == BBS_ACT_GELU; }
+static_assert(bbs::kActSilu == BBS_ACT_SILU && bbs::kActGelu == BBS_ACT_GELU, "activation codes");
+
+bool dtype_ok(int32_t d) { return d == BBS_OUT_F32 || d == BBS_OUT_BF16; }
+
+// An output the kernels write in 16-byte pieces.
+int check_rows_out(const void *p, int32_t dtype, int64_t cols, int64_t ld, const char *name) {
+    if (!p) return fail(BBS_EINVAL, "null %s", name);
+    if (!dtype_ok(dtype)) return fail(BBS_EINVAL, "bad dtype of %s", name);
+    const int64_t es = dtype == BBS_OUT_BF16 ? 2 : 4;
+    if (ld < cols || (ld * es) % 16 || !aligned(p, 16))
+        return fail(BBS_EINVAL, "%s must be 16-byte aligned with a row stride >= %lld, stride * size %% 16 == 0",
+                    name, (long long)cols);
+    return BBS_OK;
+}
+
+// Shared checks of nvfp4_gemv (Wu null) and nvfp4_gated_gemv.
+int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
+              const void *Wu, bool gated, int32_t act, void *y, int32_t y_dtype, int64_t ldy,
+              void *stream) {
+    int st;
+    if (!x) return fail(BBS_EINVAL, "null x");
+    if (!y) return fail(BBS_EINVAL, "null y");
+    if (!dtype_ok(y_dtype)) return fail(BBS_EINVAL, "bad y_dtype");
+    if (gated && !act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (tokens < 1 || tokens > BBS_GEMV_MAX_TOKENS)
+        return fail(BBS_EINVAL, "tokens must be in [1, %d]", BBS_GEMV_MAX_TOKENS);
+    bbs::GemvParams p{};
+    if (fmt == BBS_FMT_NVFP4) {
+        const bbs_fp4 *w[2] = {static_cast<const bbs_fp4 *>(W), static_cast<const bbs_fp4 *>(Wu)};
+        for (int i = 0; i < (gated ? 2 : 1); ++i) {
+            if ((st = check_fp4(w[i], i ? "Wu" : "W", true))) return st;
+            if (w[i]->sdec_per_row) return fail(BBS_ENOTSUP, "weights with a per-row decode scale");
+            p.codes[i] = w[i]->codes;
+            p.scales[i] = w[i]->scales;
+            p.s_dec[i] = w[i]->s_dec;
+        }
+        if (gated && (w[0]->rows != w[1]->rows || w[0]->cols != w[1]->cols))
+            return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
+        if (gated && w[0]->tile2d != w[1]->tile2d)
+            return fail(BBS_ENOTSUP, "Wg and Wu with different tile2d");
+        p.N = w[0]->rows;
+        p.K = w[0]->cols;
+        p.tile2d = w[0]->tile2d;
+    } else if (fmt == BBS_FMT_MXFP4) {
+        const bbs_mx4 *w[2] = {static_cast<const bbs_mx4 *>(W), static_cast<const bbs_mx4 *>(Wu)};
+        for (int i = 0; i < (gated ? 2 : 1); ++i) {
+            if ((st = check_mx4(w[i], i ? "Wu" : "W"))) return st;
+            p.codes[i] = w[i]->codes;
+            p.scales[i] = w[i]->scales;
+        }
+        if (gated && (w[0]->rows != w[1]->rows || w[0]->cols != w[1]->cols))
+            return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
+        p.N = w[0]->rows;
+        p.K = w[0]->cols;
+    } else {
+        return fail(BBS_EINVAL, "fmt must be BBS_FMT_NVFP4 or BBS_FMT_MXFP4");
+    }
+    if (ldx < p.K || ldx % 8) return fail(BBS_EINVAL, "ldx must be >= K and a multiple of 8");
+    if (!aligned(x, 16)) return fail(BBS_EINVAL, "x not 16-byte aligned");
+    if (ldy < p.N) return fail(BBS_EINVAL, "output row stride < N");
+    if (!aligned(y, y_dtype == BBS_OUT_BF16 ? 2 : 4)) return fail(BBS_EINVAL, "y not aligned to its type");
+    if ((p.N + 3) / 4 > INT32_MAX) return fail(BBS_ENOTSUP, "too many weight rows");
+    p.x = x;
+    p.T = tokens;
+    p.ldx = ldx;
+    p.y = y;
+    p.ldy = ldy;
+    return hip_status(bbs::launch_gemv(p, fmt == BBS_FMT_MXFP4, gated ? act : -1, y_dtype == BBS_OUT_BF16,
+                                       reinterpret_cast<hipStream_t>(stream)),
+                      "gemv launch");
+}
+
+}  // namespace
+
+int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W, void *y,
+               int32_t y_dtype, int64_t ldy, void *stream) {
+    g_err[0] = 0;
+    return gemv_impl(fmt, x, tokens, ldx, W, nullptr, false, 0, y, y_dtype, ldy, stream);
+}
+
+int nvfp4_gated_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *Wg,
+                     const void *Wu, int32_t act, void *h, int32_t h_dtype, int64_t ldh,
+                     void *stream) {
+    g_err[0] = 0;
+    return gemv_impl(fmt, x, tokens, ldx, Wg, Wu, true, act, h, h_dtype, ldh, stream);
+}
+
+int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act, void *H,
+                     int32_t h_dtype, int64_t ldh, const bbs_mx8 *g8, const bbs_mx8 *u8, void *stream) {
+    g_err[0] = 0;
+    int st;
+    if ((st = check_fp4(A, "A", true))) return st;
+    if ((st = check_fp4(Wg, "Wg", true))) return st;
+    if ((st = check_fp4(Wu, "Wu", true))) return st;
+    if (!act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (A->cols != Wg->cols) return fail(BBS_EINVAL, "A.cols != Wg.cols");
+    if (Wg->rows != Wu->rows || Wg->cols != Wu->cols)
+        return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
+    if (Wg->sdec_per_row || Wu->sdec_per_row)
+        return fail(BBS_ENOTSUP, "weights with a per-row decode scale");
+    if (Wg->tile2d != Wu->tile2d) return fail(BBS_ENOTSUP, "Wg and Wu with different tile2d");
+    if ((st = check_rows_out(H, h_dtype, Wg->rows, ldh, "H"))) return st;
+    if (!g8 != !u8) return fail(BBS_EINVAL, "g8 and u8 come together");
+    bbs::GatedParams p{};
+    if (g8) {
+        for (const bbs_mx8 *c : {g8, u8}) {
+            if ((st = check_mx8(c, c == g8 ? "g8" : "u8"))) return st;
+            if (c->rows != A->rows || c->cols != Wg->rows)
+                return fail(BBS_EINVAL, "g8 and u8 must be A.rows x Wg.rows");
+        }
+        p.g_codes = g8->codes;
+        p.g_scales = g8->scales;
+        p.u_codes = u8->codes;
+        p.u_scales = u8->scales;
+    }
+    p.a = {A->codes, A->scales, A->s_dec, A->rows, A->tile2d, A->sdec_per_row};
+    p.b = {Wg->codes, Wg->scales, Wg->s_dec, Wg->rows, Wg->tile2d, 0};
+    p.u = {Wu->codes, Wu->scales, Wu->s_dec, Wu->rows, Wu->tile2d, 0};
+    p.M = A->rows;
+    p.N = Wg->rows;
+    p.K = A->cols;
+    p.h = H;
+    p.ldh = ldh;
+    return hip_status(bbs::launch_gated_gemm(p, act, h_dtype == BBS_OUT_BF16,
+                                             reinterpret_cast<hipStream_t>(stream)),
+                      "gated gemm launch");
+}
+
+int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8, const bbs_mx8 *u8,
+                         int32_t act, void *dG, void *dU, int32_t dtype, int64_t ld, void *stream) {
+    g_err[0] = 0;
+    int st;
+    if ((st = check_mx8(dY, "dY"))) return st;
+    if ((st = check_mx8(Wt, "Wt"))) return st;
+    if ((st = check_mx8(g8, "g8"))) return st;
+    if ((st = check_mx8(u8, "u8"))) return st;
+    if (!act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (dY->cols != Wt->cols) return fail(BBS_EINVAL, "dY.cols != Wt.cols");
+    for (const bbs_mx8 *c : {g8, u8})
+        if (c->rows != dY->rows || c->cols != Wt->rows)
+            return fail(BBS_EINVAL, "g8 and u8 must be dY.rows x Wt.rows");
+    if ((st = check_rows_out(dG, dtype, Wt->rows, ld, "dG"))) return st;
+    if ((st = check_rows_out(dU, dtype, Wt->rows, ld, "dU"))) return st;
+    bbs::GatedBwdParams p{};
+    p.mm.a_codes = dY->codes;
+    p.mm.a_scales = dY->scales;
+    p.mm.b_codes = Wt->codes;
+    p.mm.b_scales = Wt->scales;
+    p.mm.M = dY->rows;
+    p.mm.N = Wt->rows;
+    p.mm.K = dY->cols;
+    p.mm.c = dG;
+    p.mm.ldc = ld;
+    p.g_codes = g8->codes;
+    p.g_scales = g8->scales;
+    p.u_codes = u8->codes;
+    p.u_scales = u8->scales;
+    p.du = dU;
+    return hip_status(bbs::launch_gated_bwd(p, act, dtype == BBS_OUT_BF16,
+                                            reinterpret_cast<hipStream_t>(stream)),
+                      "gated backward launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,95 @@
+// Device code the gated feed-forward kernels share after their products:
+// 8-bit checkpoints of a 32-column block, reading them back, output stores.
+#pragma once
+
+#include "bbs_device.hpp"
+#include "gated.hpp"
+
+namespace bbs {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// A transposed 32 x 32 product block: lane l holds row l % 32 and columns
+// 8 (v / 4) + 4 (l / 32) + v % 4, so lanes l and l ^ 32 hold a row's 32
+// columns between them, i.e. one MXFP8 block of a checkpoint.
+
+__device__ __forceinline__ void scale16(f32x16 &v, float s) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= s;
+}
+
+// MXFP8 codes of the lane's 16 values (word q: columns 8 q + 4 (l / 32)) and
+// the block's E8M0 byte, as the quantizer's MXFP8 copy to nearest.
+__device__ __forceinline__ uint32_t checkpoint16(const f32x16 &v, uint32_t (&w)[4]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(v[i]));
+    a = fmaxf(a, __shfl_xor(a, 32, 64));
+    const uint32_t byte = e8m0_byte(a);
+    const float scale = e8m0_cvt_scale(byte);
+    // byte 0 (2^-127) is converted at 2^-126 after doubling
+    const float twice = byte ? 1.0f : 2.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        w[q] = e4m3_rne4_scaled(v[4 * q] * twice, v[4 * q + 1] * twice, v[4 * q + 2] * twice,
+                                v[4 * q + 3] * twice, scale);
+    return byte;
+}
+
+// Row m, first column n = block + 4 (l / 32) of an M x N checkpoint; N is a
+// multiple of 32, so a block is wholly in or out.
+__device__ __forceinline__ void store_checkpoint(const uint32_t (&w)[4], uint32_t byte,
+                                                 uint8_t *codes, uint8_t *scales, int64_t N,
+                                                 int64_t m, int64_t n, int lane) {
+    if (n >= N) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(codes + m * N + n + 8 * q) = w[q];
+    if (lane < 32) scales[m * (N / 32) + n / 32] = (uint8_t)byte;
+}
+
+template <bool BF16_OUT>
+__device__ __forceinline__ void store4(void *base, int64_t at, float y0, float y1, float y2, float y3) {
+    if (BF16_OUT)
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(base) + at) =
+            make_uint2(pk_bf16(y0, y1), pk_bf16(y2, y3));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + at) = make_float4(y0, y1, y2, y3);
+}
+
+// 2^(byte - 127), an FP32 subnormal for byte 0.
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+}
+
+// Four E4M3 codes of a word times the block scale (each product exact but
+// for FP32 subnormals).
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float (&v)[4]) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, 1.0f, false);
+    const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, 1.0f, true);
+    v[0] = lo[0] * scale;
+    v[1] = lo[1] * scale;
+    v[2] = hi[0] * scale;
+    v[3] = hi[1] * scale;
+}
+
+// Four consecutive columns of one row through the gated activation's
+// backward pass: dh times u act'(g) and act(g), stored to dgate and dup.
+template <int ACT, bool BF16_OUT, typename Acc>
+__device__ __forceinline__ void gated_bwd4(const GatedBwdParams &p, int64_t m, int64_t n, const Acc &dh) {
+    const int64_t N = p.mm.N, at = m * N + n, bl = m * (N / 32) + n / 32;
+    float g[4], u[4], dg[4], du[4];
+    decode4(*reinterpret_cast<const uint32_t *>(p.g_codes + at), e8m0_value(p.g_scales[bl]), g);
+    decode4(*reinterpret_cast<const uint32_t *>(p.u_codes + at), e8m0_value(p.u_scales[bl]), u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float slope;
+        const float a = gate_act_grad<ACT>(g[e], slope);
+        dg[e] = dh[e] * u[e] * slope;
+        du[e] = dh[e] * a;
+    }
+    store4<BF16_OUT>(p.mm.c, m * p.mm.ldc + n, dg[0], dg[1], dg[2], dg[3]);
+    store4<BF16_OUT>(p.du, m * p.mm.ldc + n, du[0], du[1], du[2], du[3]);
+}
+
+}  // namespace bbs

@@ -45,6 +45,13 @@ extern "C" {
 enum bbs_round { BBS_RTN = 0, BBS_SR = 1 };
 enum bbs_out_dtype { BBS_OUT_F32 = 0, BBS_OUT_BF16 = 1 };
 enum bbs_fmt { BBS_FMT_NVFP4 = 0, BBS_FMT_MXFP8 = 1, BBS_FMT_MXFP4 = 2 };
+/* Activation of a gated feed-forward block, act(g) = g * sigma(z), sigma(z) =
+ * 1 / (1 + e^-z): SiLU has z = g; GELU (tanh form) has
+ * z = 2 sqrt(2/pi) (g + 0.044715 g^3). */
+enum bbs_act { BBS_ACT_SILU = 0, BBS_ACT_GELU = 1 };
+
+/* Most tokens nvfp4_gemv and nvfp4_gated_gemv take in one call. */
+#define BBS_GEMV_MAX_TOKENS 64
 
 /* Words of device workspace nvfp4_quantize needs for its amax partials. */
 #define BBS_AMAX_WS_FLOATS 11264
@@ -325,6 +332,59 @@ int grouped_nvfp4_gemm_s2f6(const bbs_fp4 *A, const int32_t *row_index,
                             const int64_t *group_offsets, int32_t G, int64_t max_rows,
                             const bbs_fp4 *B, int64_t N, int32_t rht, uint32_t signs,
                             const bbs_s2f6 *Y, void *stream);
+
+/* Gated up projections of a feed-forward block in one kernel:
+ *   g = A * Wg^T, u = A * Wu^T (as nvfp4_gemm, in FP32, never stored),
+ *   H = act(g) * u, computed in FP32 and rounded once to h_dtype.
+ * A is M x K; Wg and Wu are F x K with the same tile2d (one decode scale
+ * each).  H is M x F with row stride ldh (>= F) elements, 16-byte aligned,
+ * ldh * size % 16 == 0.
+ * g8 and u8 (both or neither) receive 8-bit checkpoints of g and u for
+ * mxfp8_gemm_gated_bwd: the MXFP8 copies of the FP32 values, M x F (F % 32
+ * == 0), rounded to nearest even as the row_mx8 copy of nvfp4_quantize.
+ * Products and checkpointed values must be finite.  K % 128 == 0 with 8-byte
+ * aligned scales is the fast case.  A may have a decode scale per row.
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale
+ * or with different tile2d. */
+int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act,
+                     void *H, int32_t h_dtype, int64_t ldh, const bbs_mx8 *g8,
+                     const bbs_mx8 *u8, void *stream);
+
+/* Backward pass of H = act(g) * u behind a down projection, from the 8-bit
+ * checkpoints, in one kernel: with dH = dY * Wt^T (as the MXFP8 nvfp4_gemm,
+ * in FP32, never stored) and g, u decoded from g8, u8,
+ *   dG = dH * u * act'(g),   dU = dH * act(g),
+ * computed in FP32 and rounded once to dtype.  dY is M x K (the gradient of
+ * the block's output), Wt is F x K (the down projection's weight transposed,
+ * e.g. by mxfp8_requantize_t), g8 and u8 are M x F.  dG and dU are M x F
+ * with the same row stride ld (>= F) elements, 16-byte aligned, ld * size %
+ * 16 == 0; they may be the two halves of one M x 2F matrix (ld = 2F), the
+ * row operand of the weights' gradient and of the block's input gradient.
+ * act as for the forward pass.  K % 128 == 0 with 4-byte aligned scales is
+ * the fast case.  Errors: BBS_EINVAL. */
+int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8,
+                         const bbs_mx8 *u8, int32_t act, void *dG, void *dU, int32_t dtype,
+                         int64_t ld, void *stream);
+
+/* Matrix-vector products with 4-bit weights: y = x * W^T for 1 to
+ * BBS_GEMV_MAX_TOKENS tokens (rows of x), BF16 activations that are not
+ * quantized, FP32 sums of exact products, one rounding to y_dtype.
+ *   fmt == BBS_FMT_NVFP4: W is a const bbs_fp4 * (1x16 or 16x16 scales, one
+ *      decode scale), fmt == BBS_FMT_MXFP4: a const bbs_mx4 *.
+ * x is tokens x K (BF16 patterns, row stride ldx elements, ldx % 8 == 0,
+ * 16-byte aligned), W is N x K, y is tokens x N with row stride ldy (>= N)
+ * elements.  The order of the sums depends on the sizes alone, so the same
+ * call gives the same bits.  Errors: BBS_EINVAL; BBS_ENOTSUP for a weight
+ * with a per-row decode scale. */
+int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
+               void *y, int32_t y_dtype, int64_t ldy, void *stream);
+
+/* nvfp4_gated_gemm for a few tokens, with activations as nvfp4_gemv:
+ * h = act(x * Wg^T) * (x * Wu^T).  Wg and Wu are F x K of the same format
+ * and, for NVFP4, the same tile2d (else BBS_ENOTSUP). */
+int nvfp4_gated_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *Wg,
+                     const void *Wu, int32_t act, void *h, int32_t h_dtype, int64_t ldh,
+                     void *stream);
 
 /* Name of a status code. */
 const char *bbs_strerror(int status);

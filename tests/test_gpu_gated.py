@@ -1,0 +1,455 @@
+"""The gated feed-forward operators (nvfp4_gated_gemm, mxfp8_gemm_gated_bwd,
+nvfp4_gemv, nvfp4_gated_gemv) against their definition in 64 bits over the
+oracle's decoded operands.  A sum of K exact products in FP32 is off by at most
+(K + 32) 2^-24 sum |a b| (any order, block scaling and the joining of split
+sums included); what the activation and the products add is bounded in
+gated_ref.py, and BF16 outputs must lie in the rounding of that window."""
+import numpy as np
+import pytest
+
+import oracle as O
+from gated_ref import ULP, act64, act_error, act_slope64, gated_bound, slope_error
+from gpu_util import (announce, bf16_bits_to_f64, bf16_key, bf16_bits_of, bf16_window, dev, host, to_dev,
+                      upload_mxfp8, upload_nvfp4)
+from workloads import synth
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+SENTINEL = 0x4D4D
+
+
+@pytest.fixture(scope="module")
+def bbs():
+    import bit_block_scaled_amd as b
+    return b
+
+
+def product(a, b):
+    """a b^T in 64 bits and its FP32 accumulation bound."""
+    K = a.shape[1]
+    return a @ b.T, (K + 32) * ULP * (np.abs(a) @ np.abs(b).T)
+
+
+def product_mx8(a, b):
+    """a b^T and the bound of the scaled FP8 matrix instruction: it adds each
+    aligned group of eight products on a grid 2^-13 below the group's largest
+    (test_fp8_group_grid), dropping what lies below, so a group is off by at most
+    7 steps of 2^-13 max |a b| <= 7 * 2^-13 * max |a| max |b|; groups are added
+    in FP32."""
+    M, K = a.shape
+    ref, E = product(a, b)
+    ga, gb = (np.abs(v).reshape(len(v), K // 8, 8).max(-1) for v in (a, b))
+    return ref, E + 7 * 2.0 ** -13 * (ga @ gb.T)
+
+
+def output(rows, cols, bf16, pad=0):
+    """A sentinel-filled output with `pad` columns behind each row, and one row behind the last."""
+    t = torch.full((rows + 1, (cols + pad) * (1 if bf16 else 2)), SENTINEL, dtype=torch.int16, device=dev())
+    full = t if bf16 else t.view(torch.float32)
+    return full, full[:rows, :cols]
+
+
+def values(t, bf16):
+    h = host(t)
+    return bf16_bits_to_f64(h.view(np.uint16)) if bf16 else h.astype(np.float64)
+
+
+def check(full, rows, cols, bf16, ref, E, what):
+    y = values(full[:rows, :cols].contiguous(), bf16)
+    if bf16:
+        lo, hi = bf16_window(ref, E)
+        k = bf16_key(bf16_bits_of(y))
+        bad = np.argwhere((k < lo) | (k > hi))
+    else:
+        bad = np.argwhere(~(np.abs(y - ref) <= E))
+    print(f"  {what}: rel {O.rel_fro(y, ref):.2e}", flush=True)
+    assert bad.size == 0, (what, len(bad), bad[0], y[tuple(bad[0])], ref[tuple(bad[0])], E[tuple(bad[0])])
+    raw = host(full).view(np.uint16).reshape(rows + 1, -1)
+    w = cols * (1 if bf16 else 2)
+    assert np.all(raw[rows] == SENTINEL) and np.all(raw[:rows, w:] == SENTINEL), f"{what}: wrote outside"
+
+
+def weight(bbs, fmt, N, K, seed, tile2d=False):
+    """(device tensor, its values in 64 bits)."""
+    wb = synth.normal(N, K, seed, K ** -0.5)
+    if fmt == "mxfp4":
+        q = O.mxfp4_quantize(wb)
+        return bbs.MXFP4Tensor(to_dev(q.codes), to_dev(q.scales), N, K), q.dequant_f64()
+    q = O.nvfp4_quantize(wb, tile2d=tile2d)
+    return upload_nvfp4(q, bbs), q.dequant_f64()
+
+
+def tokens(T, K, seed, pad=0):
+    """BF16 activations with `pad` columns behind each row: (device view, values in 64 bits)."""
+    xb = synth.normal_with_outliers(T, K + pad, seed)
+    return to_dev(xb)[:, :K], bf16_bits_to_f64(xb[:, :K])
+
+
+FMTS = {"nvfp4": 0, "mxfp4": 2}
+
+# tokens, rows, K, format, 16x16 scales, BF16 output, padding
+GEMV = [
+    (1, 16, 16, "nvfp4", False, False, 0),
+    (1, 16, 16, "nvfp4", True, True, 8),
+    (1, 1, 32, "mxfp4", False, False, 0),
+    (2, 5, 96, "mxfp4", False, True, 8),
+    (3, 48, 272, "nvfp4", False, False, 24),
+    (4, 1536, 528, "nvfp4", True, True, 0),
+    (5, 4112, 1552, "nvfp4", False, True, 8),
+    (7, 112, 1040, "nvfp4", True, False, 0),
+    (8, 333, 4064, "mxfp4", False, False, 0),
+    (1, 4096, 14336, "nvfp4", False, False, 0),
+    (16, 272, 2064, "nvfp4", False, True, 0),
+    (17, 96, 96, "mxfp4", False, True, 16),
+    (31, 160, 1008, "nvfp4", True, False, 8),
+    (33, 208, 2064, "nvfp4", False, True, 0),
+    (48, 97, 4096, "mxfp4", False, True, 0),
+    (64, 512, 4096, "nvfp4", True, False, 8),
+    (64, 16, 16, "nvfp4", False, True, 8),
+]
+
+
+@pytest.mark.parametrize("T,N,K,fmt,tile2d,bf16,pad", GEMV)
+def test_gemv(bbs, T, N, K, fmt, tile2d, bf16, pad):
+    announce(f"gemv {T} x {N} x {K} {fmt} tile2d={tile2d} bf16={bf16}")
+    W, w = weight(bbs, fmt, N, K, 11, tile2d)
+    x, xv = tokens(T, K, 12, pad)
+    full, y = output(T, N, bf16, pad)
+    bbs.nvfp4_gemv(FMTS[fmt], x, W, y, int(bf16))
+    torch.cuda.synchronize()
+    ref, E = product(xv, w)
+    check(full, T, N, bf16, ref, E, "y")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("T,N,K,fmt,tile2d,bf16,pad", GEMV[::2] + [(1, 1536, 4096, "nvfp4", True, True, 0),
+                                                                  (13, 208, 4096, "mxfp4", False, False, 0)])
+def test_gated_gemv(bbs, T, N, K, fmt, tile2d, bf16, pad, act):
+    announce(f"gated gemv {T} x {N} x {K} {fmt} tile2d={tile2d} bf16={bf16} {act}")
+    Wg, wg = weight(bbs, fmt, N, K, 21, tile2d)
+    Wu, wu = weight(bbs, fmt, N, K, 22, tile2d)
+    x, xv = tokens(T, K, 23, pad)
+    full, h = output(T, N, bf16, pad)
+    bbs.nvfp4_gated_gemv(FMTS[fmt], x, Wg, Wu, h, int(bf16), act=int(act == "gelu"))
+    torch.cuda.synchronize()
+    (g, Eg), (u, Eu) = product(xv, wg), product(xv, wu)
+    check(full, T, N, bf16, act64(act, g) * u, gated_bound(act, g, u, Eg, Eu), "h")
+
+
+def identity16(bbs):
+    """The 16 x 16 identity as an NVFP4 tensor (code 1.0, scale 1)."""
+    codes = np.zeros((16, 8), np.uint8)
+    for i in range(16):
+        codes[i, i // 2] = 2 << (4 * (i % 2))
+    return bbs.NVFP4Tensor(to_dev(codes), to_dev(np.full((16, 1), 0x38, np.uint8)),
+                           to_dev(np.ones(1, np.float32)), 16, 16, False)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activation_over_its_range(bbs, act):
+    """Identity weights make g = u = x exactly: h = x act(x) at BF16 values of every binade and sign."""
+    announce(f"activation range {act}")
+    mag = (np.arange(512) * 33 + 7) % 0x5F00             # up to 2^62: x act(x) stays finite
+    bits = np.concatenate([mag, mag | 0x8000]).astype(np.uint16).reshape(64, 16)
+    x = bf16_bits_to_f64(bits)
+    I = identity16(bbs)
+    full, h = output(64, 16, False)
+    bbs.nvfp4_gated_gemv(0, to_dev(bits), I, I, h, 0, act=int(act == "gelu"))
+    torch.cuda.synchronize()
+    E = np.abs(x) * act_error(act, x) + 2 * ULP * np.abs(x * act64(act, x)) + 2.0 ** -125 * (1 + np.abs(x))
+    check(full, 64, 16, False, x * act64(act, x), E, act)
+
+
+def test_gemv_tokens_do_not_mix(bbs):
+    """A token's infinities and NaN stay in its own row; a zero row gives zeros."""
+    for T, bad in ((3, 1), (16, 15), (20, 17)):
+        announce(f"gemv isolation {T}")
+        N, K = 48, 544
+        W, w = weight(bbs, "nvfp4", N, K, 31)
+        xb = synth.normal_with_outliers(T, K, 32)
+        clean = bf16_bits_to_f64(xb)
+        xb[bad, 3], xb[bad, 500] = 0x7F80, 0x7FC0
+        xb[0] = 0
+        clean[0] = 0
+        full, y = output(T, N, False)
+        bbs.nvfp4_gemv(0, to_dev(xb), W, y, 0)
+        torch.cuda.synchronize()
+        ref, E = product(clean, w)
+        got = host(y).astype(np.float64)
+        assert np.all(np.isnan(got[bad]))
+        keep = np.arange(T) != bad
+        assert np.all(np.abs(got[keep] - ref[keep]) <= E[keep])
+        assert np.all(got[0] == 0)
+
+
+def test_gemv_extreme_scales(bbs):
+    """The smallest and largest block scales, every code, and a tiny decode scale."""
+    announce("gemv extreme scales")
+    N, K, T = 32, 288, 6
+    rng = np.random.default_rng(5)
+    codes = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    scales = rng.choice(np.array([0x01, 0x07, 0x08, 0x38, 0x7E, 0x00], np.uint8), (N, K // 16))
+    s_dec = np.array([2.0 ** -40], np.float32)
+    q = O.NVFP4(codes, scales, s_dec[0], N, K, False)
+    W = bbs.NVFP4Tensor(to_dev(codes), to_dev(scales), to_dev(s_dec), N, K, False)
+    x, xv = tokens(T, K, 33)
+    full, y = output(T, N, False)
+    bbs.nvfp4_gemv(0, x, W, y, 0)
+    ms = rng.choice(np.array([1, 60, 127, 140, 200], np.uint8), (N, K // 32))
+    m = O.MXFP4(codes, ms, N, K)
+    fullm, ym = output(T, N, False)
+    bbs.nvfp4_gemv(2, x, bbs.MXFP4Tensor(to_dev(codes), to_dev(ms), N, K), ym, 0)
+    torch.cuda.synchronize()
+    check(full, T, N, False, *product(xv, q.dequant_f64()), "nvfp4")
+    check(fullm, T, N, False, *product(xv, m.dequant_f64()), "mxfp4")
+
+
+def test_gemv_offsets_beyond_32_bits(bbs):
+    """Code bytes past 4 GiB: the last rows of a tall matrix."""
+    announce("gemv past 4 GiB")
+    N, K, T = 131104, 65552, 2                            # 4.3e9 code bytes
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=dev())
+    scales = torch.full((N, K // 16), 0x38, dtype=torch.uint8, device=dev())
+    assert codes.numel() > 2 ** 32
+    W64, w = weight(bbs, "nvfp4", 64, K, 41)
+    codes[-64:], scales[-64:] = W64.codes, W64.scales
+    x, xv = tokens(T, K, 42)
+    y = torch.full((T, N), 7.0, dtype=torch.float32, device=dev())
+    bbs.nvfp4_gemv(0, x, bbs.NVFP4Tensor(codes, scales, W64.s_dec, N, K, False), y, 0)
+    torch.cuda.synchronize()
+    ref, E = product(xv, w)
+    assert np.all(np.abs(host(y[:, -64:]).astype(np.float64) - ref) <= E)
+    assert float(y[:, :-64].abs().max()) == 0.0
+
+
+# M, F, K, 16x16 weight scales, per-token A scale, act, BF16, checkpoints, padding
+FWD = [
+    (16, 16, 16, False, False, "silu", False, False, 0),
+    (16, 32, 128, True, False, "gelu", True, True, 8),
+    (48, 112, 272, False, False, "silu", True, False, 8),
+    (272, 1568, 1184, False, False, "gelu", True, True, 0),
+    (528, 336, 1552, False, False, "silu", False, False, 16),
+    (256, 512, 1024, True, False, "silu", True, True, 0),
+    (304, 160, 512, False, True, "gelu", False, True, 8),
+    (16, 1536, 4096, True, False, "silu", True, True, 0),
+    (1040, 288, 256, True, False, "silu", False, True, 0),
+    (32, 96, 96, False, True, "silu", True, True, 0),
+]
+
+
+def nvfp4_rows(bbs, M, K, seed, per_token):
+    xb = synth.normal_with_outliers(M, K, seed)
+    if not per_token:
+        q = O.nvfp4_quantize(xb)
+        return upload_nvfp4(q, bbs), q.dequant_f64()
+    q = O.nvfp4_quantize_act(xb, per_token=True, four_six=False)
+    return bbs.NVFP4Tensor(to_dev(q.codes), to_dev(q.scales), to_dev(np.asarray(q.s_dec, np.float32)), M, K,
+                           False, sdec_per_row=True), q.dequant_f64()
+
+
+def check_checkpoint(t, ref, E, what):
+    """MXFP8 codes of values within E of ref: each 32-block's scale is the one the
+    rule gives for some amax in the window, and each value is within half an
+    E4M3 step (2^-4 of the value, or 2^-10 of the scale) of the window."""
+    M, N = ref.shape
+    q = O.MXFP8(host(t.codes), host(t.scales), M, N)
+    v = q.dequant_f64()
+    k = host(t.scales).astype(np.int64) - 127
+    a = np.abs(ref).reshape(M, N // 32, 32).max(-1)
+    e = E.reshape(M, N // 32, 32).max(-1)
+    assert np.all(448 * np.exp2(k.astype(np.float64)) >= a - e), f"{what}: a block overflows its scale"
+    small = 448 * np.exp2(k - 1.0) >= a + e
+    assert not np.any(small & (k > -127)), f"{what}: a block's scale is larger than it need be"
+    unit = np.repeat(np.exp2(k.astype(np.float64)), 32, axis=1)
+    half = np.maximum((np.abs(ref) + E) * 2.0 ** -4, unit * 2.0 ** -10)
+    assert np.all(np.abs(v - ref) <= half + E), f"{what}: a value is more than half a step off"
+    # away from the rounding borders the codes are the oracle's
+    same = O.mxfp8_encode_f32(ref.astype(np.float32)).codes == host(t.codes)
+    assert same.mean() > 0.99, f"{what}: {1 - same.mean():.3f} of the codes differ"
+
+
+@pytest.mark.parametrize("M,F,K,tile2d,per_token,act,bf16,ckpt,pad", FWD)
+def test_gated_gemm(bbs, M, F, K, tile2d, per_token, act, bf16, ckpt, pad):
+    announce(f"gated gemm {M} x {F} x {K} tile2d={tile2d} per_token={per_token} {act} bf16={bf16} ckpt={ckpt}")
+    A, a = nvfp4_rows(bbs, M, K, 51, per_token)
+    Wg, wg = weight(bbs, "nvfp4", F, K, 52, tile2d)
+    Wu, wu = weight(bbs, "nvfp4", F, K, 53, tile2d)
+    full, h = output(M, F, bf16, pad)
+    c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) if ckpt else None for _ in range(2)]
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, int(bf16), act=int(act == "gelu"), g_ckpt=c[0], u_ckpt=c[1])
+    torch.cuda.synchronize()
+    (g, Eg), (u, Eu) = product(a, wg), product(a, wu)
+    check(full, M, F, bf16, act64(act, g) * u, gated_bound(act, g, u, Eg, Eu), "h")
+    if ckpt:
+        check_checkpoint(c[0], g, Eg, "g8")
+        check_checkpoint(c[1], u, Eu, "u8")
+
+
+def test_checkpoint_of_zero_and_tiny_rows(bbs):
+    """All-zero blocks get scale byte 0 and zero codes; FP32-subnormal products the smallest scales."""
+    announce("checkpoints of zero and tiny values")
+    M, F, K = 32, 64, 128
+    A, _ = nvfp4_rows(bbs, M, K, 54, False)
+    Wg, wg = weight(bbs, "nvfp4", F, K, 55)
+    Wu, _ = weight(bbs, "nvfp4", F, K, 56)
+    a = host(A.codes).copy()
+    a[:16] = 0
+    A = bbs.NVFP4Tensor(to_dev(a), A.scales, A.s_dec, M, K, False)
+    A.s_dec.fill_(2.0 ** -120)
+    Wg.s_dec.fill_(2.0 ** -14)
+    Wu.s_dec.fill_(1.0)
+    full, h = output(M, F, False)
+    c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) for _ in range(2)]
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, 0, g_ckpt=c[0], u_ckpt=c[1])
+    torch.cuda.synchronize()
+    for t in c:
+        assert int(t.scales[:16].max()) == 0
+        assert int((t.codes[:16] & 0x7F).max()) == 0
+    q = O.NVFP4(a, host(A.scales), np.float32(2.0 ** -120), M, K, False)
+    w = O.NVFP4(host(Wg.codes), host(Wg.scales), np.float32(2.0 ** -14), F, K, False)
+    g = q.dequant_f64() @ w.dequant_f64().T
+    got = O.MXFP8(host(c[0].codes), host(c[0].scales), M, F).dequant_f64()
+    # the smallest E4M3 step at scale 2^-127 is 2^-136; FP32 subnormals step 2^-149
+    assert np.all(np.abs(got - g) <= np.maximum(np.abs(g) * 2.0 ** -4, 2.0 ** -137) + 2.0 ** -147)
+    assert float(h.abs().max()) <= 2.0 ** -100
+
+
+BWD = [
+    (1, 32, 32, "silu", False, 0),
+    (24, 96, 64, "gelu", True, 8),
+    (16, 256, 128, "silu", True, 0),
+    (1000, 1568, 1056, "gelu", True, 0),
+    (300, 544, 512, "silu", False, 8),
+    (257, 288, 1184, "silu", True, 16),
+    (512, 768, 384, "gelu", False, 0),
+]
+
+
+@pytest.mark.parametrize("M,F,K,act,bf16,pad", BWD)
+def test_gated_bwd(bbs, M, F, K, act, bf16, pad):
+    announce(f"gated bwd {M} x {F} x {K} {act} bf16={bf16}")
+    oy = O.mxfp8_quantize(synth.laplace(M, K, 61, 1e-2), mode=O.RTN)
+    ow = O.mxfp8_quantize(synth.normal(F, K, 62, F ** -0.5), mode=O.RTN)
+    og = O.mxfp8_quantize(synth.normal(M, F, 63, 2.0), mode=O.RTN)
+    ou = O.mxfp8_quantize(synth.normal(M, F, 64, 1.0), mode=O.RTN)
+    es = 1 if bf16 else 2
+    buf = torch.full((M + 1, (2 * F + pad) * es), SENTINEL, dtype=torch.int16, device=dev())
+    buf = buf if bf16 else buf.view(torch.float32)
+    dg, du = buf[:M, :F], buf[:M, F:2 * F]
+    bbs.mxfp8_gemm_gated_bwd(upload_mxfp8(oy, bbs), upload_mxfp8(ow, bbs), upload_mxfp8(og, bbs),
+                             upload_mxfp8(ou, bbs), dg, du, int(bf16), act=int(act == "gelu"))
+    torch.cuda.synchronize()
+    dh, Ed = product_mx8(oy.dequant_f64(), ow.dequant_f64())
+    g, u = og.dequant_f64(), ou.dequant_f64()
+    a, sl = act64(act, g), act_slope64(act, g)
+    ea, es_ = act_error(act, g), slope_error(act, g)
+    tiny = 2.0 ** -140
+    E_g = np.abs(u) * ((np.abs(dh) + Ed) * es_ + np.abs(sl) * Ed) + 3 * ULP * np.abs(dh * u * sl) + tiny
+    E_u = (np.abs(dh) + Ed) * ea + np.abs(a) * Ed + 2 * ULP * np.abs(dh * a) + tiny
+    check(buf, M, 2 * F, bf16, np.concatenate([dh * u * sl, dh * a], 1), np.concatenate([E_g, E_u], 1), "dg, du")
+
+
+def test_bwd_is_the_gradient_of_the_forward_pass(bbs):
+    """Central differences of sum(dH * h) through the forward kernel's own
+    formula at the checkpointed values match dG and dU."""
+    announce("gated bwd against differences")
+    M, F, K = 64, 64, 64
+    oy = O.mxfp8_quantize(synth.laplace(M, K, 71, 1e-2), mode=O.RTN)
+    ow = O.mxfp8_quantize(synth.normal(F, K, 72, F ** -0.5), mode=O.RTN)
+    og = O.mxfp8_quantize(synth.normal(M, F, 73, 2.0), mode=O.RTN)
+    ou = O.mxfp8_quantize(synth.normal(M, F, 74, 1.0), mode=O.RTN)
+    dg, du = (torch.empty((M, F), dtype=torch.float32, device=dev()) for _ in range(2))
+    for act in ("silu", "gelu"):
+        bbs.mxfp8_gemm_gated_bwd(upload_mxfp8(oy, bbs), upload_mxfp8(ow, bbs), upload_mxfp8(og, bbs),
+                                 upload_mxfp8(ou, bbs), dg, du, 0, act=int(act == "gelu"))
+        dh, Ed = product_mx8(oy.dequant_f64(), ow.dequant_f64())
+        g, u, e = og.dequant_f64(), ou.dequant_f64(), 1e-5
+        fg = dh * (act64(act, g + e) - act64(act, g - e)) * u / (2 * e)
+        fu = dh * act64(act, g) * ((u + e) - (u - e)) / (2 * e)
+        # a difference is off by 8 e^2 / 6 and by the rounding of the values over e; the kernel by
+        # its product and at most 64 FP32 roundings of terms below (1 + |g|) (1 + |u|) |dh|
+        size = (1 + np.abs(g)) * (1 + np.abs(u))
+        tol = 1.2 * size * Ed + np.abs(dh) * size * (64 * ULP + 2 * e * e + 2.0 ** -50 / e)
+        for got, ref in ((dg, fg), (du, fu)):
+            assert np.all(np.abs(host(got).astype(np.float64) - ref) <= tol), act
+
+
+def test_fp8_group_grid(bbs):
+    """The scaled FP8 matrix instruction keeps a product beside one of 2^16 in its
+    aligned group of eight when it is at least 2^3, and drops a smaller one; in
+    another group everything FP32 holds is kept.  (The bound of the MXFP8
+    products above rests on this.)"""
+    announce("FP8 matrix instruction: grid of a group of eight")
+    K = 128
+    e = np.arange(-6, 16)
+    code = lambda x: ((np.asarray(x) + 7) << 3).astype(np.uint8)          # E4M3 code of 2^x, x in [-6, 8]
+    for place in (1, 5, 7, 8, 31, 100):
+        ea = np.minimum(e, 8)
+        a = np.zeros((len(e), K), np.uint8)
+        a[:, 0], a[:, place] = code(8), code(ea)
+        for sign in (0, 0x80):
+            b = np.zeros((16, K), np.uint8)
+            b[:, 0] = code(8)
+            got = []
+            for i in range(len(e)):
+                bi = b.copy()
+                bi[:, place] = code(e[i] - ea[i]) | sign
+                c = torch.empty((1, 16), dtype=torch.float32, device=dev())
+                one = np.full((1, K // 32), 127, np.uint8)
+                bbs.nvfp4_gemm(1, bbs.MXFP8Tensor(to_dev(a[i:i + 1]), to_dev(one), 1, K),
+                               bbs.MXFP8Tensor(to_dev(bi), to_dev(np.repeat(one, 16, 0)), 16, K), c, 0)
+                got.append(c[0, 0])
+            got = host(torch.stack(got)).astype(np.float64) - 65536
+            kept = np.where((e >= 3) | (place >= 8), np.exp2(e.astype(np.float64)), 0.0) * (-1 if sign else 1)
+            assert np.array_equal(got, kept), (place, sign, got, kept)
+
+
+def test_streams_and_graphs(bbs):
+    """The operators on a side stream, and captured together into a graph that
+    is replayed with new inputs, give the eager bits."""
+    announce("gated operators: stream and graph")
+    M, F, K = 64, 256, 256
+    A, _ = nvfp4_rows(bbs, M, K, 81, False)
+    Wg, _ = weight(bbs, "nvfp4", F, K, 82, True)
+    Wu, _ = weight(bbs, "nvfp4", F, K, 83, True)
+    Wt = upload_mxfp8(O.mxfp8_quantize(synth.normal(F, K, 84, F ** -0.5), mode=O.RTN), bbs)
+    dY = upload_mxfp8(O.mxfp8_quantize(synth.laplace(M, K, 85, 1e-2), mode=O.RTN), bbs)
+    x, _ = tokens(5, K, 86)
+
+    def buffers():
+        return {"h": torch.empty((M, F), dtype=torch.bfloat16, device=dev()),
+                "d": torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev()),
+                "v": torch.empty((5, F), dtype=torch.bfloat16, device=dev()),
+                "y": torch.empty((5, F), dtype=torch.float32, device=dev()),
+                "c": [bbs.MXFP8Tensor.empty(M, F, device=dev()) for _ in range(2)]}
+
+    def calls(b):
+        bbs.nvfp4_gated_gemm(A, Wg, Wu, b["h"], 1, g_ckpt=b["c"][0], u_ckpt=b["c"][1])
+        bbs.mxfp8_gemm_gated_bwd(dY, Wt, *b["c"], b["d"][:, :F], b["d"][:, F:], 1)
+        bbs.nvfp4_gated_gemv(0, x, Wg, Wu, b["v"], 1)
+        bbs.nvfp4_gemv(0, x, Wg, b["y"], 0)
+
+    def same(a, b):
+        return all(torch.equal(a[k], b[k]) for k in ("h", "d", "v", "y")) and all(
+            torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales) for p, q in zip(a["c"], b["c"]))
+
+    eager, side, cap = buffers(), buffers(), buffers()
+    calls(eager)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        calls(side)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    assert same(eager, side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(cap)
+    for r in range(4):
+        x.copy_(torch.roll(x, 1, 0))
+        A.codes.copy_(torch.roll(A.codes, 3, 0))
+        graph.replay()
+        calls(eager)
+        torch.cuda.synchronize()
+        assert same(eager, cap), r
