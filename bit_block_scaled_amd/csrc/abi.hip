@@ -700,9 +700,7 @@ int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const
         for (int i = 0; i < (gated ? 2 : 1); ++i) {
             if ((st = check_fp4(w[i], i ? "Wu" : "W", true))) return st;
             if (w[i]->sdec_per_row) return fail(BBS_ENOTSUP, "weights with a per-row decode scale");
-            p.codes[i] = w[i]->codes;
-            p.scales[i] = w[i]->scales;
-            p.s_dec[i] = w[i]->s_dec;
+            (i ? p.u : p.w) = {w[i]->codes, w[i]->scales, w[i]->s_dec};
         }
         if (gated && (w[0]->rows != w[1]->rows || w[0]->cols != w[1]->cols))
             return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
@@ -715,8 +713,7 @@ int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const
         const bbs_mx4 *w[2] = {static_cast<const bbs_mx4 *>(W), static_cast<const bbs_mx4 *>(Wu)};
         for (int i = 0; i < (gated ? 2 : 1); ++i) {
             if ((st = check_mx4(w[i], i ? "Wu" : "W"))) return st;
-            p.codes[i] = w[i]->codes;
-            p.scales[i] = w[i]->scales;
+            (i ? p.u : p.w) = {w[i]->codes, w[i]->scales, nullptr};
         }
         if (gated && (w[0]->rows != w[1]->rows || w[0]->cols != w[1]->cols))
             return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
@@ -729,14 +726,17 @@ int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const
     if (!aligned(x, 16)) return fail(BBS_EINVAL, "x not 16-byte aligned");
     if (ldy < p.N) return fail(BBS_EINVAL, "output row stride < N");
     if (!aligned(y, y_dtype == BBS_OUT_BF16 ? 2 : 4)) return fail(BBS_EINVAL, "y not aligned to its type");
-    if ((p.N + 3) / 4 > INT32_MAX) return fail(BBS_ENOTSUP, "too many weight rows");
+    // row offsets inside a workgroup's 64 rows are 32 bits wide
+    if (p.N > INT32_MAX || p.K > (int64_t)1 << 26)
+        return fail(BBS_ENOTSUP, "weights of more than 2^31 - 1 rows or 2^26 columns");
     p.x = x;
     p.T = tokens;
     p.ldx = ldx;
     p.y = y;
     p.ldy = ldy;
-    return hip_status(bbs::launch_gemv(p, fmt == BBS_FMT_MXFP4, gated ? act : -1, y_dtype == BBS_OUT_BF16,
-                                       reinterpret_cast<hipStream_t>(stream)),
+    p.bf16_out = y_dtype == BBS_OUT_BF16;
+    p.act = gated ? act : -1;
+    return hip_status(bbs::launch_gemv(p, fmt == BBS_FMT_MXFP4, reinterpret_cast<hipStream_t>(stream)),
                       "gemv launch");
 }
 

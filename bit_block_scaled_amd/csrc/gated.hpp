@@ -35,18 +35,21 @@ struct GatedBwdParams {
 struct GemvParams {
     const uint16_t *x;
     int64_t T, ldx;
-    const uint8_t *codes[2], *scales[2];
-    const float *s_dec[2];         // null for MXFP4
+    struct Weight {
+        const uint8_t *codes, *scales;
+        const float *s_dec;        // null for MXFP4
+    } w, u;                        // u: the up weights of the gated form
     int64_t N, K;
     int tile2d;
     void *y;
     int64_t ldy;
+    int bf16_out;
+    int act;                       // < 0: one matrix, y = x W^T; else the gated form of the two
 };
 
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
-// act < 0: one matrix, y = x W^T; otherwise the gated form of the two.
-hipError_t launch_gemv(const GemvParams &p, bool mxfp4, int act, bool bf16_out, hipStream_t s);
+hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s);
 
 // e^-z within a few FP32 ulp for every z: the product with log2 e is carried
 // in two parts (the hardware exponential rounds to one ulp), so the relative

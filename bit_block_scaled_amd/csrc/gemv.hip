@@ -11,7 +11,7 @@
 // order, so enough waves are in flight also where N is small.  The matrix
 // instructions take the BF16 activations as they are; E2M1 codes are exact in
 // BF16, so only the FP32 sums round.
-#include <type_traits>
+#include <algorithm>
 
 #include "bbs_device.hpp"
 #include "gated_epilogue.hpp"
@@ -42,12 +42,21 @@ __device__ __forceinline__ uint32_t load_bytes(const uint8_t *p) {
     return v;
 }
 
-// One output from its sums: decode scales, activation, one rounding.
-template <bool MX, int ACT, bool BF16_OUT>
-__device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n, float v0, float v1) {
-    float y = MX ? v0 : v0 * p.s_dec[0][0];
-    if constexpr (ACT >= 0) y = gate_act<ACT>(y) * (MX ? v1 : v1 * p.s_dec[1][0]);
-    if (BF16_OUT) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(y, y);
+// Layout of the block scales.
+constexpr int kRows16 = 0;       // NVFP4, one E4M3 byte per 16 weights of a row
+constexpr int kTiles16 = 1;      // NVFP4, one E4M3 byte per 16 x 16 weights
+constexpr int kRows32 = 2;       // MXFP4, one E8M0 byte per 32 weights of a row
+
+// One output from its sums: decode scales, activation, one rounding.  The
+// activation and the output type are the same for every lane.
+template <int SC, int NM>
+__device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n, const float (&v)[2]) {
+    float y = SC == kRows32 ? v[0] : v[0] * p.w.s_dec[0];
+    if constexpr (NM == 2) {
+        const float u = SC == kRows32 ? v[1] : v[1] * p.u.s_dec[0];
+        y = (p.act == kActSilu ? gate_act<kActSilu>(y) : gate_act<kActGelu>(y)) * u;
+    }
+    if (p.bf16_out) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(y, y);
     else static_cast<float *>(p.y)[t * p.ldy + n] = y;
 }
 
@@ -65,48 +74,95 @@ __device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n
 // ---------------------------------------------------------------------------
 constexpr int kStepK = 512;
 
-template <bool MX, int NM, int NG, int R>
+template <int NM, int NG, int R>
 struct Step {
     uint4 w[NM][R];          // 32 codes
     uint32_t s[NM][R];       // two E4M3 bytes or one E8M0 byte
     uint4 x[NG][4];          // 32 activations of one token
 };
 
-template <bool MX, int NM, int NG, int R>
-__device__ __forceinline__ void load_step(Step<MX, NM, NG, R> &st, const GemvParams &p, int64_t n0,
-                                          int64_t step) {
-    const int lane = threadIdx.x & 63, i = lane & 3;
-    const int64_t k = step * kStepK + (lane >> 2) * 32;
-    // K is a multiple of 16: a lane has both its 16-value halves, the first, or none
-    const bool first = k < p.K, second = k + 16 < p.K;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+// The lane's places in a step, set once: byte offsets of its rows from the
+// workgroup's first row, and its tokens' activations.
+template <int NG, int R>
+struct Place {
+    uint32_t code[R], scale[R];
+    const uint16_t *x[NG];
+};
+
+template <int SC, int NM, int NG, int R>
+__device__ __forceinline__ Place<NG, R> place_of(const GemvParams &p, int64_t n0) {
+    Place<NG, R> pl;
+    const int lane = threadIdx.x & 63, i = lane & 3, b = lane >> 2;
 #pragma unroll
-    for (int w = 0; w < NM; ++w)
+    for (int r = 0; r < R; ++r) {
+        // MXFP4 has any number of rows: the last one stands in past the end
+        const uint32_t row = SC == kRows32 ? (uint32_t)min((int64_t)(4 * r + i), p.N - 1 - n0) : 4 * r + i;
+        pl.code[r] = row * (uint32_t)(p.K / 2) + b * 16;
+        pl.scale[r] = SC == kRows16   ? row * (uint32_t)(p.K / 16) + b * 2
+                      : SC == kRows32 ? row * (uint32_t)(p.K / 32) + b
+                                      : b * 2;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) pl.x[g] = p.x + min((int64_t)(4 * g + i), p.T - 1) * p.ldx + b * 32;
+    return pl;
+}
+
+// TAIL: the step K ends in; a lane then has both its 16-value halves, the
+// first, or none.  It loads the halves from wherever they are or, past the
+// end, from the row's last one, and clears what does not belong to it: no
+// load waits behind a branch.
+template <int SC, int NM, int NG, int R, bool TAIL>
+__device__ __forceinline__ void load_step(Step<NM, NG, R> &st, const GemvParams &p,
+                                          const Place<NG, R> &pl, int64_t n0, int64_t step) {
+    const int b = (threadIdx.x & 63) >> 2;
+    const int64_t k0 = step * kStepK;
+    // TAIL: the lane's halves (16-value units from k0) as loaded
+    const int left = TAIL ? (int)(p.K - k0) / 16 : 32;
+    const int h0 = min(2 * b, left - 1), h1 = min(2 * b + 1, left - 1);
+    const bool first = 2 * b < left, second = 2 * b + 1 < left;
+#pragma unroll
+    for (int w = 0; w < NM; ++w) {
+        const GemvParams::Weight &W = w ? p.u : p.w;
+        const uint8_t *cb = W.codes + n0 * (p.K / 2) + k0 / 2;
+        const uint8_t *sb = W.scales + (SC == kRows16   ? n0 * (p.K / 16) + k0 / 16
+                                        : SC == kRows32 ? n0 * (p.K / 32) + k0 / 32
+                                                        : n0 / 16 * (p.K / 16) + k0 / 16);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int64_t n = min(n0 + 4 * r + i, p.N - 1);
-            const uint8_t *c = p.codes[w] + n * (p.K / 2) + k / 2;
-            st.w[w][r] = zero;
-            st.s[w][r] = 0;
-            if (second) st.w[w][r] = *reinterpret_cast<const uint4 *>(c);
-            else if (first) {
-                const uint2 h = *reinterpret_cast<const uint2 *>(c);
-                st.w[w][r].x = h.x;
-                st.w[w][r].y = h.y;
-            }
-            if (MX) {
-                if (first) st.s[w][r] = load_bytes<1>(p.scales[w] + n * (p.K / 32) + k / 32);
+            if (!TAIL) {
+                st.w[w][r] = *reinterpret_cast<const uint4 *>(cb + pl.code[r]);
             } else {
-                const uint8_t *s = p.scales[w] + (p.tile2d ? n / 16 : n) * (p.K / 16) + k / 16;
-                if (second) st.s[w][r] = load_bytes<2>(s);
-                else if (first) st.s[w][r] = load_bytes<1>(s);
+                const uint8_t *row = cb + pl.code[r] - 16 * b;
+                const uint2 c0 = *reinterpret_cast<const uint2 *>(row + 8 * h0);
+                const uint2 c1 = *reinterpret_cast<const uint2 *>(row + 8 * h1);
+                st.w[w][r] = make_uint4(first ? c0.x : 0, first ? c0.y : 0, second ? c1.x : 0, second ? c1.y : 0);
+            }
+            if (SC == kTiles16 && r > 0) {
+                st.s[w][r] = st.s[w][0];                 // the workgroup's rows share a tile row
+            } else if (SC == kRows32) {
+                const uint8_t *s = sb + pl.scale[r];
+                st.s[w][r] = load_bytes<1>(TAIL ? s - b + h0 / 2 : s);
+            } else if (!TAIL) {
+                st.s[w][r] = load_bytes<2>(sb + pl.scale[r]);
+            } else {
+                const uint8_t *s = sb + pl.scale[r] - 2 * b;
+                st.s[w][r] = load_bytes<1>(s + h0) | load_bytes<1>(s + h1) << 8;
             }
         }
+    }
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + min((int64_t)(4 * g + i), p.T - 1) * p.ldx + k);
+        const uint4 *xr = reinterpret_cast<const uint4 *>(pl.x[g] + k0) - 4 * (TAIL ? b : 0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) st.x[g][q] = (q < 2 ? first : second) ? xr[q] : zero;
+        for (int q = 0; q < 4; ++q) {
+            if (!TAIL) {
+                st.x[g][q] = xr[q];
+            } else {
+                const uint4 v = xr[2 * (q < 2 ? h0 : h1) + (q & 1)];
+                const bool in = q < 2 ? first : second;
+                st.x[g][q] = make_uint4(in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0);
+            }
+        }
     }
 }
 
@@ -125,9 +181,8 @@ __device__ __forceinline__ s16x4 codes4(uint32_t w, int h) {
 }
 
 // TT tokens are computed (1, 2, 4 or 8), those from p.T on are not stored.
-template <bool MX, int NM, int TT, int R>
-__device__ __forceinline__ void add_step(float (&acc)[NM][R][TT],
-                                         const Step<MX, NM, (TT + 3) / 4, R> &st) {
+template <int SC, int NM, int TT, int R>
+__device__ __forceinline__ void add_step(float (&acc)[NM][R][TT], const Step<NM, (TT + 3) / 4, R> &st) {
     constexpr int NG = (TT + 3) / 4, NT = TT < 4 ? TT : 4;
 #pragma unroll
     for (int hb = 0; hb < 2; ++hb)                       // the lane's two 16-value halves
@@ -138,8 +193,7 @@ __device__ __forceinline__ void add_step(float (&acc)[NM][R][TT],
                 s16x4 cw[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) cw[q] = codes4(word(st.w[w][r], 2 * hb + (q >> 1)), q & 1);
-                const uint32_t sb = MX ? st.s[w][r] : (st.s[w][r] >> (8 * hb)) & 0xFFu;
-                const float sc = MX ? e8m0_value(sb) : e4m3_value(sb);
+                const float sc = SC == kRows32 ? e8m0_value(st.s[w][r]) : e4m3_value(st.s[w][r] >> (8 * hb));
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -164,26 +218,34 @@ __device__ __forceinline__ float sum_blocks(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-constexpr int kMaxSplit = 16;            // waves of a workgroup (K splits)
+constexpr int kFewSplit = 8;     // most waves of a workgroup (K splits)
 
-template <bool MX, int ACT, bool BF16_OUT, int TT, int R>
-__global__ __launch_bounds__(64 * kMaxSplit) void gemv_few_kernel(GemvParams p) {
-    constexpr int NM = ACT >= 0 ? 2 : 1, NG = (TT + 3) / 4, NS = NM * R * TT * 4;
-    __shared__ float part[kMaxSplit][NS];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+template <int SC, int NM, int TT, int R>
+__global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) {
+    constexpr int NG = (TT + 3) / 4, NO = TT * R * 4;    // outputs, of NM sums each
+    __shared__ float part[kFewSplit][NM * NO];
+    const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * (4 * R);
-    const int64_t steps = (p.K + kStepK - 1) / kStepK;
+    const int64_t full = p.K / kStepK;
+    const Place<NG, R> pl = place_of<SC, NM, NG, R>(p, n0);
     float acc[NM][R][TT] = {};
-    for (int64_t s = wave; s < steps; s += 2 * nw) {
-        Step<MX, NM, NG, R> a, b;
-        load_step<MX, NM, NG, R>(a, p, n0, s);
-        if (s + nw < steps) {
-            load_step<MX, NM, NG, R>(b, p, n0, s + nw);
-            add_step<MX, NM, TT, R>(acc, a);
-            add_step<MX, NM, TT, R>(acc, b);
-        } else {
-            add_step<MX, NM, TT, R>(acc, a);
+    int64_t s = wave;
+    if (s < full) {
+        Step<NM, NG, R> cur, nxt;
+        load_step<SC, NM, NG, R, false>(cur, p, pl, n0, s);
+        for (; s + nw < full; s += nw) {
+            load_step<SC, NM, NG, R, false>(nxt, p, pl, n0, s + nw);
+            add_step<SC, NM, TT, R>(acc, cur);
+            cur = nxt;
         }
+        add_step<SC, NM, TT, R>(acc, cur);
+        s += nw;
+    }
+    if (s == full && p.K % kStepK) {
+        Step<NM, NG, R> last;
+        load_step<SC, NM, NG, R, true>(last, p, pl, n0, s);
+        add_step<SC, NM, TT, R>(acc, last);
     }
 #pragma unroll
     for (int w = 0; w < NM; ++w)
@@ -192,17 +254,16 @@ __global__ __launch_bounds__(64 * kMaxSplit) void gemv_few_kernel(GemvParams p) 
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
                 const float v = sum_blocks(acc[w][r][t]);
-                if (lane < 4) part[wave][((w * TT + t) * R + r) * 4 + lane] = v;
+                if (lane < 4) part[wave][w * NO + (t * R + r) * 4 + lane] = v;
             }
     __syncthreads();
-    constexpr int NO = TT * R * 4;       // outputs, of NM sums each
     for (int o = threadIdx.x; o < NO; o += blockDim.x) {
         float v[2] = {0.0f, 0.0f};
         for (int k = 0; k < nw; ++k)
 #pragma unroll
             for (int w = 0; w < NM; ++w) v[w] += part[k][w * NO + o];
         const int64_t t = o / (R * 4), n = n0 + o % (R * 4);
-        if (t < p.T && n < p.N) finish<MX, ACT, BF16_OUT>(p, t, n, v[0], v[1]);
+        if (t < p.T && n < p.N) finish<SC, NM>(p, t, n, v);
     }
 }
 
@@ -210,17 +271,24 @@ __global__ __launch_bounds__(64 * kMaxSplit) void gemv_few_kernel(GemvParams p) 
 // Nine tokens and more: v_mfma_f32_16x16x32_bf16, sixteen weight rows by
 // sixteen tokens.  Code x scale is exact in BF16 (at most 6 significant bits
 // for E2M1 x E4M3), so the weights are expanded once and serve every token
-// tile.  A wave's step is 256 K values: lane 16 g + i reads 32 bytes (64
-// codes) of row i and 64 activations of token i at K offset 64 g, which feed
-// eight instructions.
+// tile.  A wave's step is 128 K values of its row tiles: lane 16 g + i reads
+// 16 bytes (32 codes) of row i at K offset 32 g, which feed four instructions.
+//
+// The activations of a step go to the wave's own part of LDS (NT x 16 tokens x
+// 256 bytes, asynchronous copies of whole token rows): taken straight to
+// registers in the instructions' layout every lane would touch another cache
+// line, and with 48 tokens those loads took longer than the weights'.  In LDS
+// the 16-byte chunk c of token i lies at place c ^ i, so the sixteen lanes of
+// one fragment read fall on sixteen different bank groups.
 // ---------------------------------------------------------------------------
-constexpr int kTileK = 256;
+constexpr int kTileK = 128;
 constexpr int kTileSplit = 8;
 
-template <bool MX>
+// Eight codes of a word times their block scale, in BF16.
+template <int SC>
 __device__ __forceinline__ bf16x8 expand8(uint32_t w, float sc) {
     uint32_t o[4];
-    if constexpr (MX) {
+    if constexpr (SC == kRows32) {
         o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 0));
         o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 1));
         o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, sc, 2));
@@ -238,16 +306,104 @@ __device__ __forceinline__ bf16x8 expand8(uint32_t w, float sc) {
     return __builtin_bit_cast(bf16x8, make_uint4(o[0], o[1], o[2], o[3]));
 }
 
+template <int NM, int NR>
+struct TileWeights {
+    uint4 c[NM][NR];
+    uint32_t s[NM][NR];                  // two E4M3 bytes or one E8M0 byte
+};
+
+template <int NR>
+struct TilePlace {
+    uint32_t code[NR], scale[NR];        // from the workgroup's first row
+};
+
+// TAIL: as for the few-token step, the lane's two 16-value halves are loaded
+// from inside K and cleared where they lie past it.
+template <int SC, int NM, int NR, bool TAIL>
+__device__ __forceinline__ void load_weights(TileWeights<NM, NR> &tw, const GemvParams &p,
+                                             const TilePlace<NR> &pl, int64_t n0, int64_t k0) {
+    const int g = (threadIdx.x & 63) >> 4;
+    const int left = TAIL ? (int)(p.K - k0) / 16 : 8;
+    const int h0 = min(2 * g, left - 1), h1 = min(2 * g + 1, left - 1);
+    const bool first = 2 * g < left, second = 2 * g + 1 < left;
+#pragma unroll
+    for (int w = 0; w < NM; ++w) {
+        const GemvParams::Weight &W = w ? p.u : p.w;
+        const uint8_t *cb = W.codes + n0 * (p.K / 2) + k0 / 2;
+        const uint8_t *sb = W.scales + (SC == kRows16   ? n0 * (p.K / 16) + k0 / 16
+                                        : SC == kRows32 ? n0 * (p.K / 32) + k0 / 32
+                                                        : n0 / 16 * (p.K / 16) + k0 / 16);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            if (!TAIL) {
+                tw.c[w][r] = *reinterpret_cast<const uint4 *>(cb + pl.code[r]);
+                tw.s[w][r] = SC == kRows32 ? load_bytes<1>(sb + pl.scale[r]) : load_bytes<2>(sb + pl.scale[r]);
+            } else {
+                const uint8_t *row = cb + pl.code[r] - 16 * g;
+                const uint2 c0 = *reinterpret_cast<const uint2 *>(row + 8 * h0);
+                const uint2 c1 = *reinterpret_cast<const uint2 *>(row + 8 * h1);
+                tw.c[w][r] = make_uint4(first ? c0.x : 0, first ? c0.y : 0, second ? c1.x : 0, second ? c1.y : 0);
+                if (SC == kRows32) {
+                    tw.s[w][r] = load_bytes<1>(sb + pl.scale[r] - g + h0 / 2);
+                } else {
+                    const uint8_t *s = sb + pl.scale[r] - 2 * g;
+                    tw.s[w][r] = load_bytes<1>(s + h0) | load_bytes<1>(s + h1) << 8;
+                }
+            }
+        }
+    }
+}
+
+// The products of one step; x(t, j): chunk j of the lane's eight activations
+// for token tile t.
+template <int SC, int NM, int NT, int NR, typename X>
+__device__ __forceinline__ void tile_products(f32x4 (&acc)[NM][NR][NT], const TileWeights<NM, NR> &tw, X x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        bf16x8 xf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xf[t] = x(t, j);
+#pragma unroll
+        for (int w = 0; w < NM; ++w)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float sc = SC == kRows32 ? e8m0_value(tw.s[w][r]) : e4m3_value(tw.s[w][r] >> (8 * (j >> 1)));
+                const bf16x8 a = expand8<SC>(word(tw.c[w][r], j), sc);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[w][r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, xf[t], acc[w][r][t], 0, 0, 0);
+            }
+    }
+}
+
 // NT token tiles, NR row tiles of each matrix.
-template <bool MX, int ACT, bool BF16_OUT, int NT, int NR>
+template <int SC, int NM, int NT, int NR>
 __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p) {
-    constexpr int NM = ACT >= 0 ? 2 : 1;
     constexpr int NO = NR * NT * 256;                     // sums of one matrix
-    extern __shared__ __align__(16) float tile_part[];    // [wave][matrix][row tile][token tile][lane][4]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+    // the waves' activations, then their sums [wave][matrix][row tile][token tile][lane][4]
+    extern __shared__ __align__(16) uint8_t tile_lds[];
+    const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * NR);
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    TilePlace<NR> pl;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const uint32_t row = (uint32_t)min((int64_t)(16 * r + i), p.N - 1 - n0);
+        pl.code[r] = row * (uint32_t)(p.K / 2) + 16 * g;
+        pl.scale[r] = SC == kRows16   ? row * (uint32_t)(p.K / 16) + 2 * g
+                      : SC == kRows32 ? row * (uint32_t)(p.K / 32) + g
+                                      : row / 16 * (uint32_t)(p.K / 16) + 2 * g;
+    }
+    // copy q of a step: tokens 4 q .. 4 q + 3, lane l the chunk that belongs at
+    // place l % 16 of token 4 q + l / 16
+    uint8_t *const xl = tile_lds + wave * (NT * 4096);
+    const uint16_t *src[4 * NT];
+#pragma unroll
+    for (int q = 0; q < 4 * NT; ++q) {
+        const int t = 4 * q + g;
+        src[q] = p.x + min((int64_t)t, p.T - 1) * p.ldx + 8 * (i ^ (t & 15));
+    }
     f32x4 acc[NM][NR][NT];
 #pragma unroll
     for (int w = 0; w < NM; ++w)
@@ -256,59 +412,31 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[w][r][t] = f32x4{0, 0, 0, 0};
 
-    for (int64_t k = (int64_t)wave * kTileK + 64 * g; k - 64 * g < p.K; k += (int64_t)nw * kTileK) {
-        // the lane's 16-value blocks that lie inside K: 4, or fewer at the end
-        const int64_t left = (p.K - k) / 16;
-        const int nb = left < 0 ? 0 : left > 4 ? 4 : (int)left;
-        uint4 cw[NM][NR][2], xv[NT][8];
-        uint32_t sw[NM][NR];
+    TileWeights<NM, NR> tw;
+    int64_t k0 = (int64_t)wave * kTileK;
+    for (; k0 + kTileK <= p.K; k0 += (int64_t)nw * kTileK) {
+        load_weights<SC, NM, NR, false>(tw, p, pl, n0, k0);
+        // the wave's reads of the step before are done
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int w = 0; w < NM; ++w)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                const int64_t n = min(n0 + 16 * r + i, p.N - 1);
-                const uint8_t *c = p.codes[w] + n * (p.K / 2) + k / 2;
-                const uint8_t *s = MX ? p.scales[w] + n * (p.K / 32) + k / 32
-                                      : p.scales[w] + (p.tile2d ? n / 16 : n) * (p.K / 16) + k / 16;
-                cw[w][r][0] = cw[w][r][1] = zero;
-                sw[w][r] = 0;
-                if (nb == 4) {
-                    cw[w][r][0] = reinterpret_cast<const uint4 *>(c)[0];
-                    cw[w][r][1] = reinterpret_cast<const uint4 *>(c)[1];
-                    sw[w][r] = MX ? load_bytes<2>(s) : load_bytes<4>(s);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < 3; ++b)
-                        if (b < nb) {
-                            const uint2 h = reinterpret_cast<const uint2 *>(c)[b];
-                            if (b & 1) cw[w][r][b >> 1].z = h.x, cw[w][r][b >> 1].w = h.y;
-                            else cw[w][r][b >> 1].x = h.x, cw[w][r][b >> 1].y = h.y;
-                            if (!MX) sw[w][r] |= load_bytes<1>(s + b) << (8 * b);
-                            else if (!(b & 1)) sw[w][r] |= load_bytes<1>(s + b / 2) << (4 * b);
-                        }
-                }
-            }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const uint4 *xr = reinterpret_cast<const uint4 *>(p.x + min((int64_t)(16 * t + i), p.T - 1) * p.ldx + k);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) xv[t][q] = q < 2 * nb ? xr[q] : zero;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-#pragma unroll
-            for (int w = 0; w < NM; ++w)
-#pragma unroll
-                for (int r = 0; r < NR; ++r) {
-                    const uint32_t sb = (sw[w][r] >> (8 * (MX ? q >> 2 : q >> 1))) & 0xFFu;
-                    const bf16x8 a = expand8<MX>(word(cw[w][r][q >> 2], q & 3),
-                                                 MX ? e8m0_value(sb) : e4m3_value(sb));
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        acc[w][r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            a, __builtin_bit_cast(bf16x8, xv[t][q]), acc[w][r][t], 0, 0, 0);
-                }
+        for (int q = 0; q < 4 * NT; ++q) copy_lds16(src[q] + k0, xl + q * 1024);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        tile_products<SC, NM, NT, NR>(acc, tw, [&](int t, int j) {
+            return *reinterpret_cast<const bf16x8 *>(xl + (16 * t + i) * 256 + 16 * ((4 * g + j) ^ i));
+        });
     }
+    if (k0 < p.K) {
+        load_weights<SC, NM, NR, true>(tw, p, pl, n0, k0);
+        const int left = (int)(p.K - k0) / 8;             // chunks of a token inside K
+        tile_products<SC, NM, NT, NR>(acc, tw, [&](int t, int j) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(
+                p.x + min((int64_t)(16 * t + i), p.T - 1) * p.ldx + k0 + 8 * min(4 * g + j, left - 1));
+            const bool in = 4 * g + j < left;
+            return __builtin_bit_cast(bf16x8, make_uint4(in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0));
+        });
+    }
+    __syncthreads();                                      // the activations' place is reused
+    float *const part = reinterpret_cast<float *>(tile_lds);
     // lane 16 g + i holds token i of a token tile and rows 4 g .. 4 g + 3
 #pragma unroll
     for (int w = 0; w < NM; ++w)
@@ -316,86 +444,103 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
         for (int r = 0; r < NR; ++r)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                *reinterpret_cast<f32x4 *>(tile_part + (wave * NM + w) * NO + (r * NT + t) * 256 + lane * 4) =
-                    acc[w][r][t];
+                *reinterpret_cast<f32x4 *>(part + (wave * NM + w) * NO + (r * NT + t) * 256 + lane * 4) = acc[w][r][t];
     __syncthreads();
     for (int o = threadIdx.x; o < NO; o += blockDim.x) {
         float v[2] = {0.0f, 0.0f};
         for (int s = 0; s < nw; ++s)
 #pragma unroll
-            for (int w = 0; w < NM; ++w) v[w] += tile_part[(s * NM + w) * NO + o];
+            for (int w = 0; w < NM; ++w) v[w] += part[(s * NM + w) * NO + o];
         // consecutive o: rows 4 g + v of one token
         const int tile = o >> 8, l = (o >> 2) & 63;
         const int64_t t = (tile % NT) * 16 + (l & 15);
         const int64_t n = n0 + (tile / NT) * 16 + (l >> 4) * 4 + (o & 3);
-        if (t < p.T && n < p.N) finish<MX, ACT, BF16_OUT>(p, t, n, v[0], v[1]);
+        if (t < p.T && n < p.N) finish<SC, NM>(p, t, n, v);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Launch rules
 // ---------------------------------------------------------------------------
-
-template <bool MX, int ACT, bool BF16_OUT, int TT, int R>
+template <int SC, int NM, int TT, int R>
 hipError_t few(const GemvParams &p, hipStream_t s) {
     const int64_t steps = (p.K + kStepK - 1) / kStepK;
-    // two steps a wave: both are loaded before the first is used
-    const int64_t waves = steps <= 1 ? 1 : steps >= 2 * kMaxSplit ? kMaxSplit : (steps + 1) / 2;
+    // two steps a wave, both loaded before the first is used: one token, 4096
+    // x 14336: 8.1 us with 8 waves, 9.3 with 4, 8.2 with 16; 1536 x 4096: 3.2
+    // us with 4 waves, 3.1 with 8, 4.6 with 1
+    const int64_t waves = std::min<int64_t>((steps + 1) / 2, kFewSplit);
     const dim3 grid((unsigned)((p.N + 4 * R - 1) / (4 * R)));
-    hipLaunchKernelGGL((gemv_few_kernel<MX, ACT, BF16_OUT, TT, R>), grid, dim3((unsigned)(64 * waves)), 0, s, p);
+    hipLaunchKernelGGL((gemv_few_kernel<SC, NM, TT, R>), grid, dim3((unsigned)(64 * waves)), 0, s, p);
     return hipGetLastError();
 }
 
-template <bool MX, int ACT, bool BF16_OUT, int NT, int NR>
+template <int SC, int NM, int NT, int NR>
 hipError_t tile(const GemvParams &p, hipStream_t s) {
-    constexpr int NM = ACT >= 0 ? 2 : 1;
     const int64_t steps = (p.K + kTileK - 1) / kTileK;
-    const int64_t waves = steps >= kTileSplit ? kTileSplit : steps;
+    const int64_t waves = std::min<int64_t>(steps, kTileSplit);
     const dim3 grid((unsigned)((p.N + 16 * NR - 1) / (16 * NR)));
-    constexpr size_t wave_bytes = (size_t)NM * NR * NT * 1024;
+    // a wave's activations, then its sums
+    constexpr size_t wave_bytes = (size_t)NT * 1024 * (NM * NR > 4 ? NM * NR : 4);
     static const bool attr_set = [] {
-        (void)hipFuncSetAttribute(
-            reinterpret_cast<const void *>(&gemv_tile_kernel<MX, ACT, BF16_OUT, NT, NR>),
-            hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kTileSplit * wave_bytes));
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(&gemv_tile_kernel<SC, NM, NT, NR>),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)(kTileSplit * wave_bytes));
         return true;
     }();
     (void)attr_set;
-    hipLaunchKernelGGL((gemv_tile_kernel<MX, ACT, BF16_OUT, NT, NR>), grid, dim3((unsigned)(64 * waves)),
+    hipLaunchKernelGGL((gemv_tile_kernel<SC, NM, NT, NR>), grid, dim3((unsigned)(64 * waves)),
                        waves * wave_bytes, s, p);
     return hipGetLastError();
 }
 
-template <bool MX, int ACT, bool BF16_OUT>
-hipError_t run(const GemvParams &p, hipStream_t s) {
-    // rows of a workgroup: fewer for the gated form, which reads two matrices
-    constexpr int R = ACT >= 0 ? 2 : 4;
-    if (p.T <= 8) {
-        if (p.T == 1) return few<MX, ACT, BF16_OUT, 1, R>(p, s);
-        if (p.T == 2) return few<MX, ACT, BF16_OUT, 2, R>(p, s);
-        if (p.T <= 4) return few<MX, ACT, BF16_OUT, 4, R>(p, s);
-        return few<MX, ACT, BF16_OUT, 8, R>(p, s);
+// Rows of a workgroup, over both matrices of the gated form: 16 where that
+// still gives every CU one (one token, 4096 x 14336: 8.1 us with 16 rows, 8.4
+// with 8), 8 below (1536 x 4096: 3.2 us with 8 rows, 3.7 with 16, 3.4 with 4).
+// Eight tokens hold twice the sums and take 8.
+template <int SC, int NM, int TT>
+hipError_t few_rows(const GemvParams &p, hipStream_t s) {
+    const bool many = p.N >= 4096;
+    if constexpr (NM == 1) {
+        if constexpr (TT < 8)
+            if (many) return few<SC, NM, TT, 4>(p, s);
+        return few<SC, NM, TT, 2>(p, s);
+    } else {
+        return many ? few<SC, NM, TT, 2>(p, s) : few<SC, NM, TT, 1>(p, s);
     }
-    constexpr int NR = ACT >= 0 ? 1 : 2;
-    if (p.T <= 16) return tile<MX, ACT, BF16_OUT, 1, NR>(p, s);
-    if (p.T <= 32) return tile<MX, ACT, BF16_OUT, 2, NR>(p, s);
-    if (p.T <= 48) return tile<MX, ACT, BF16_OUT, 3, NR>(p, s);
-    return tile<MX, ACT, BF16_OUT, 4, NR>(p, s);
+}
+
+// Row tiles of a workgroup, over both matrices: each re-reads the activations
+// once for all its rows, so as many as leave about a workgroup a CU (48
+// tokens, MXFP4 14336 x 4096: 18.1 us with 64 rows, 23.0 with 32, 29.9 with
+// 16; gated 13 tokens 1536 x 4096: 6.9 us with 16 + 16 rows, 11.0 with 32 + 32).
+template <int SC, int NM, int NT>
+hipError_t tile_rows(const GemvParams &p, hipStream_t s) {
+    if (p.N >= 8192) return tile<SC, NM, NT, 4 / NM>(p, s);
+    if (p.N >= 4096 || NM == 2) return tile<SC, NM, NT, 2 / NM>(p, s);
+    return tile<SC, NM, NT, 1>(p, s);
+}
+
+template <int SC, int NM>
+hipError_t run(const GemvParams &p, hipStream_t s) {
+    if (p.T == 1) return few_rows<SC, NM, 1>(p, s);
+    if (p.T == 2) return few_rows<SC, NM, 2>(p, s);
+    if (p.T <= 4) return few_rows<SC, NM, 4>(p, s);
+    if (p.T <= 8) return few_rows<SC, NM, 8>(p, s);
+    if (p.T <= 16) return tile_rows<SC, NM, 1>(p, s);
+    if (p.T <= 32) return tile_rows<SC, NM, 2>(p, s);
+    if (p.T <= 48) return tile_rows<SC, NM, 3>(p, s);
+    return tile_rows<SC, NM, 4>(p, s);
+}
+
+template <int SC>
+hipError_t by_act(const GemvParams &p, hipStream_t s) {
+    return p.act < 0 ? run<SC, 1>(p, s) : run<SC, 2>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_gemv(const GemvParams &p, bool mxfp4, int act, bool bf16_out, hipStream_t s) {
-    auto pick = [&](auto mx, auto a) {
-        constexpr bool MX = decltype(mx)::value;
-        constexpr int ACT = decltype(a)::value;
-        return bf16_out ? run<MX, ACT, true>(p, s) : run<MX, ACT, false>(p, s);
-    };
-    auto by_act = [&](auto mx) {
-        if (act == kActSilu) return pick(mx, std::integral_constant<int, kActSilu>{});
-        if (act == kActGelu) return pick(mx, std::integral_constant<int, kActGelu>{});
-        return pick(mx, std::integral_constant<int, -1>{});
-    };
-    return mxfp4 ? by_act(std::true_type{}) : by_act(std::false_type{});
+hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s) {
+    if (mxfp4) return by_act<kRows32>(p, s);
+    return p.tile2d ? by_act<kTiles16>(p, s) : by_act<kRows16>(p, s);
 }
 
 }  // namespace bbs

@@ -375,7 +375,8 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
  * 16-byte aligned), W is N x K, y is tokens x N with row stride ldy (>= N)
  * elements.  The order of the sums depends on the sizes alone, so the same
  * call gives the same bits.  Errors: BBS_EINVAL; BBS_ENOTSUP for a weight
- * with a per-row decode scale. */
+ * with a per-row decode scale, or with more than 2^31 - 1 rows or 2^26
+ * columns. */
 int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
                void *y, int32_t y_dtype, int64_t ldy, void *stream);
 
