@@ -270,6 +270,9 @@ hipError_t bwd(const GatedBwdParams &p, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s) {
+    auto al8 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 8 == 0; };
+    if (p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales) && al8(p.u.scales))
+        return launch_gated_gemm_big(p, act, bf16_out, s);
     if (act == kActGelu) return bf16_out ? fwd<kActGelu, true>(p, s) : fwd<kActGelu, false>(p, s);
     return bf16_out ? fwd<kActSilu, true>(p, s) : fwd<kActSilu, false>(p, s);
 }

@@ -48,6 +48,8 @@ struct GemvParams {
 };
 
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
+// The large-tile kernel (K % 128 == 0, 16-byte aligned codes, 8-byte aligned scales).
+hipError_t launch_gated_gemm_big(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s);
 

@@ -47,6 +47,19 @@ __device__ __forceinline__ void store_checkpoint(const uint32_t (&w)[4], uint32_
     if (lane < 32) scales[m * (N / 32) + n / 32] = (uint8_t)byte;
 }
 
+// The same with the words exchanged between lanes l and l ^ 32 first: lane half
+// h then holds the block's columns 16 h .. 16 h + 15 and stores them at once.
+// n: the block's first column.  Every lane of the wave takes part.
+__device__ __forceinline__ void store_checkpoint16(const uint32_t (&w)[4], uint32_t byte, uint8_t *codes,
+                                                   uint8_t *scales, int64_t N, bool row_in, int64_t m,
+                                                   int64_t n, int half) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    if (!row_in || n >= N) return;
+    *reinterpret_cast<uint4 *>(codes + m * N + n + 16 * half) = make_uint4(a[0], a[1], b[0], b[1]);
+    if (half == 0) scales[m * (N / 32) + n / 32] = (uint8_t)byte;
+}
+
 template <bool BF16_OUT>
 __device__ __forceinline__ void store4(void *base, int64_t at, float y0, float y1, float y2, float y3) {
     if (BF16_OUT)
