@@ -142,10 +142,10 @@ __global__ __launch_bounds__(kThreads) void gated_gemm_kernel(GatedParams p) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (n + 8 * q >= p.N) continue;
-            store4<BF16_OUT>(p.h, m * p.ldh + n + 8 * q, gate_act<ACT>(g[4 * q]) * u[4 * q],
-                             gate_act<ACT>(g[4 * q + 1]) * u[4 * q + 1],
-                             gate_act<ACT>(g[4 * q + 2]) * u[4 * q + 2],
-                             gate_act<ACT>(g[4 * q + 3]) * u[4 * q + 3]);
+            store4<BF16_OUT>(p.h, m * p.ldh + n + 8 * q, gate_act<ACT, BF16_OUT>(g[4 * q]) * u[4 * q],
+                             gate_act<ACT, BF16_OUT>(g[4 * q + 1]) * u[4 * q + 1],
+                             gate_act<ACT, BF16_OUT>(g[4 * q + 2]) * u[4 * q + 2],
+                             gate_act<ACT, BF16_OUT>(g[4 * q + 3]) * u[4 * q + 3]);
         }
     }
 }
@@ -241,7 +241,10 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedBwdParams p) {
         for (int j = 0; j < 4; ++j) {
             const int64_t n = n0 + wn * 64 + j * 16 + 4 * (lane >> 4);
             if (n >= mm.N) continue;
-            gated_bwd4<ACT, BF16_OUT>(p, m, n, acc[i][j]);
+            const int64_t at = m * mm.N + n, bl = m * (mm.N / 32) + n / 32;
+            gated_bwd4<ACT, BF16_OUT>(p, m, n, acc[i][j], *reinterpret_cast<const uint32_t *>(p.g_codes + at),
+                                      p.g_scales[bl], *reinterpret_cast<const uint32_t *>(p.u_codes + at),
+                                      p.u_scales[bl]);
         }
     }
 }
@@ -278,6 +281,11 @@ hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipSt
 }
 
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
+    auto al4 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
+    // (the large tiles' row offsets are 32 bits wide)
+    const int64_t lim = (int64_t)1 << 24;
+    if (p.mm.K % 128 == 0 && p.mm.K < lim && p.mm.N < lim && al4(p.mm.a_scales) && al4(p.mm.b_scales))
+        return launch_gated_bwd_big(p, act, bf16_out, s);
     if (act == kActGelu) return bf16_out ? bwd<kActGelu, true>(p, s) : bwd<kActGelu, false>(p, s);
     return bf16_out ? bwd<kActSilu, true>(p, s) : bwd<kActSilu, false>(p, s);
 }

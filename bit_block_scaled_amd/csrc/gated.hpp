@@ -50,6 +50,8 @@ struct GemvParams {
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
 // The large-tile kernel (K % 128 == 0, 16-byte aligned codes, 8-byte aligned scales).
 hipError_t launch_gated_gemm_big(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
+// The same for the backward pass (K % 128 == 0, 4-byte aligned scales).
+hipError_t launch_gated_bwd_big(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s);
 
@@ -71,21 +73,28 @@ __device__ __forceinline__ float gate_z(float g) {
     return 1.5957691216f * __builtin_fmaf(0.044715f * (g * g), g, g);
 }
 
-// act(g) = g sigma(z), sigma(z) = 1 / (1 + e^-z).
-template <int ACT>
+// act(g) = g sigma(z), sigma(z) = 1 / (1 + e^-z).  TO_BF16: the result is
+// rounded to BF16, and the exponent's product with log2 e may round once: the
+// relative error of e^-z is then |z| 2^-24 at most, far below half a BF16 step
+// wherever e^-z matters beside 1 or the result is not negligible.
+template <int ACT, bool TO_BF16>
 __device__ __forceinline__ float gate_act(float g) {
-    return g * __builtin_amdgcn_rcpf(1.0f + exp_neg(gate_z<ACT>(g)));
+    const float z = gate_z<ACT>(g);
+    const float e = TO_BF16 ? __builtin_amdgcn_exp2f(z * -1.44269502f) : exp_neg(z);
+    return g * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // act(g) and its derivative s + g s (1 - s) dz/dg, with 1 - s taken as
-// e^-z s, which does not cancel for large z (where e^-z is infinite s is 0,
-// and so is the product: the minimum keeps it from being infinity times 0).
-template <int ACT>
+// e^-z s, which does not cancel for large z (the minimum keeps e^-z finite, so
+// that it is not infinity times 0).
+template <int ACT, bool TO_BF16>
 __device__ __forceinline__ float gate_act_grad(float g, float &slope) {
-    const float e = exp_neg(gate_z<ACT>(g));
+    const float z = gate_z<ACT>(g);
+    const float e = TO_BF16 ? __builtin_amdgcn_exp2f(fminf(z * -1.44269502f, 126.0f))
+                            : fminf(exp_neg(z), 3.0e38f);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
     const float a = g * s;
-    const float r = a * (s * fminf(e, 3.0e38f));
+    const float r = a * (s * e);
     slope = ACT == kActSilu
                 ? s + r
                 : __builtin_fmaf(r, 1.5957691216f * __builtin_fmaf(0.134145f * g, g, 1.0f), s);

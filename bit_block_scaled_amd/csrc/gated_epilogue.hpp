@@ -74,30 +74,34 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte) {
     return __uint_as_float(byte ? byte << 23 : 0x00400000u);
 }
 
-// Four E4M3 codes of a word times the block scale (each product exact but
-// for FP32 subnormals).
-__device__ __forceinline__ void decode4(uint32_t w, float scale, float (&v)[4]) {
+// Four E4M3 codes of a word times 2^(byte - 127).  The conversion takes its
+// scale from the exponent field alone, so byte 0 (2^-127) needs no other
+// encoding (measured over every code).
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t byte, float (&v)[4]) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
-    const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, 1.0f, false);
-    const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, 1.0f, true);
-    v[0] = lo[0] * scale;
-    v[1] = lo[1] * scale;
-    v[2] = hi[0] * scale;
-    v[3] = hi[1] * scale;
+    const float scale = __uint_as_float(byte << 23);
+    const f32x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, scale, false);
+    const f32x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)w, scale, true);
+    v[0] = lo[0];
+    v[1] = lo[1];
+    v[2] = hi[0];
+    v[3] = hi[1];
 }
 
 // Four consecutive columns of one row through the gated activation's
 // backward pass: dh times u act'(g) and act(g), stored to dgate and dup.
+// g_word, u_word: their checkpoint codes; g_byte, u_byte: the block scales.
 template <int ACT, bool BF16_OUT, typename Acc>
-__device__ __forceinline__ void gated_bwd4(const GatedBwdParams &p, int64_t m, int64_t n, const Acc &dh) {
-    const int64_t N = p.mm.N, at = m * N + n, bl = m * (N / 32) + n / 32;
+__device__ __forceinline__ void gated_bwd4(const GatedBwdParams &p, int64_t m, int64_t n, const Acc &dh,
+                                           uint32_t g_word, uint32_t g_byte, uint32_t u_word,
+                                           uint32_t u_byte) {
     float g[4], u[4], dg[4], du[4];
-    decode4(*reinterpret_cast<const uint32_t *>(p.g_codes + at), e8m0_value(p.g_scales[bl]), g);
-    decode4(*reinterpret_cast<const uint32_t *>(p.u_codes + at), e8m0_value(p.u_scales[bl]), u);
+    decode4(g_word, g_byte, g);
+    decode4(u_word, u_byte, u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float slope;
-        const float a = gate_act_grad<ACT>(g[e], slope);
+        const float a = gate_act_grad<ACT, BF16_OUT>(g[e], slope);
         dg[e] = dh[e] * u[e] * slope;
         du[e] = dh[e] * a;
     }

@@ -35,12 +35,12 @@
 
 #include "bbs_device.hpp"
 #include "bbs_kernels.hpp"
+#include "gated_epilogue.hpp"
 
 namespace bbs {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(1))) void gbl_void_t;
 namespace mx {
@@ -166,12 +166,12 @@ constexpr int kIssued8 = 18;
 // wave's reads are all issued; after one barrier at shell 6 the stage is free
 // and the copies of slab sn (two slabs ahead) go into it during shells 6-7:
 // they get most of two slabs to land, where copying into the other stage of a
-// two-stage ring gives them one.
+// two-stage ring gives them one.  kn: byte offset of the copied codes.
 __device__ __forceinline__ void compute_held(Stage<false> &st, f32x4 (&acc)[8][8], int wm,
-                                             int wn, int lane, const Plan &pl, int64_t sn) {
+                                             int wn, int lane, const Plan &pl, int64_t sn,
+                                             int64_t kn) {
     const int w = threadIdx.x >> 6;
     const int g = lane >> 4, rl = lane & 15;
-    const int64_t kn = sn * BK;
     i32x8 af[8], bf[8];
     // the lane's eight scale words per operand, adjacent in the stage (rows
     // rl + 16 k for k = 0-3 in one half, 4-7 in the other: swapped for rl >= 8)
@@ -223,6 +223,27 @@ __device__ __forceinline__ void compute_held(Stage<false> &st, f32x4 (&acc)[8][8
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+}
+
+// A plan whose code copies bring a 256 x 256 byte tile of an M x N byte matrix
+// into a stage instead of a slab: columns 0-127 of the tile to the A side,
+// 128-255 to the B side, each row's chunks swizzled as a slab's.  Rows and
+// columns past the matrix are clamped: they are never used.  The scale copies
+// stay the slab's.
+__device__ __forceinline__ Plan byte_tile_plan(const Plan &slab, const uint8_t *x, int64_t M, int64_t N,
+                                               int64_t m0, int64_t n0) {
+    Plan pl = slab;
+    const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+    pl.a_base = pl.b_base = x + m0 * N + n0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int row = (w * 8 + q) * 8 + (lane >> 3);
+        const int c = swz(row, lane & 7);
+        const int64_t at = (min(m0 + row, M - 1) - m0) * N;
+        pl.a_off[q] = (uint32_t)(at + min((int64_t)16 * c, N - 16 - n0));
+        pl.b_off[q] = (uint32_t)(at + min((int64_t)128 + 16 * c, N - 16 - n0));
+    }
+    return pl;
 }
 
 // FP4 slabs on v_mfma_scale_f32_32x32x64_f8f6f4, the full-rate form for
@@ -318,8 +339,17 @@ __device__ __forceinline__ void compute4_held(Stage<true> &st, f32x16 (&acc)[4][
 
 }  // namespace mx
 
-template <bool FP4, bool BF16_OUT>
-__device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *smem_raw) {
+// The FP8 product's plain epilogue.
+struct StoreC {};
+
+// Finish: StoreC, or the epilogue of an FP8 product that reads two M x N byte
+// matrices (tile0, tile1) beside the accumulators, which are laid out as
+// described where C is stored below.  The ring's last two look-ahead copies,
+// which a plain product spends on repeating its last slab, bring the tile's
+// bytes into LDS: tile 0 while the last slab is multiplied, tile 1 at its end.
+template <bool FP4, bool BF16_OUT, typename Finish = StoreC>
+__device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *smem_raw,
+                                            const Finish &finish = Finish{}) {
     mx::Smem<FP4> &sm = *reinterpret_cast<mx::Smem<FP4> *>(smem_raw);
     const int64_t tm = (p.M + mx::BM - 1) / mx::BM, tn = (p.N + mx::BN - 1) / mx::BN;
     const int64_t T = tm * tn;
@@ -351,7 +381,30 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
     }
 
     const int64_t nslab = p.K / (FP4 ? 2 * mx::BK : mx::BK);
-    if constexpr (!FP4) {
+    if constexpr (!FP4 && !std::is_same_v<Finish, StoreC>) {
+        auto tile = [&](const uint8_t *x) { return mx::byte_tile_plan(pl, x, p.M, p.N, m0, n0); };
+        mx::issue(sm.st[0], pl, 0);
+        if (nslab > 1) {
+            mx::issue(sm.st[1], pl, 1);
+        } else {
+            mx::issue(sm.st[1], tile(finish.tile0()), 0);
+        }
+        mx::wait_vmcnt<mx::kIssued8>();
+        __syncthreads();
+        __builtin_amdgcn_s_waitcnt(0xC07F);           // no scalar load in flight into the loop
+        for (int64_t s = 0; s + 2 < nslab; ++s) {
+            mx::compute_held(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK);
+            mx::wait_vmcnt<mx::kIssued8>();
+            __syncthreads();
+        }
+        if (nslab > 1) {
+            mx::compute_held(sm.st[nslab & 1], acc, wm, wn, lane, tile(finish.tile0()), 0, 0);
+            mx::wait_vmcnt<mx::kIssued8>();
+            __syncthreads();
+        }
+        mx::compute_held(sm.st[(nslab - 1) & 1], acc, wm, wn, lane, tile(finish.tile1()), 0, 0);
+        finish(sm.st[nslab & 1].a, sm.st[(nslab - 1) & 1].a, acc, m0, n0, wm, wn, lane);
+    } else if constexpr (!FP4) {
         // Slab s lives in stage s % 2 and is copied while slab s - 2 is
         // multiplied (compute_held); past the end the last slab is copied
         // again into the freed stage, which keeps the loop free of branches.
@@ -366,7 +419,7 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
         __builtin_amdgcn_s_waitcnt(0xC07F);
         for (int64_t s = 0; s < nslab; ++s) {
             const int64_t sn = s + 2 < nslab ? s + 2 : nslab - 1;
-            mx::compute_held(sm.st[s & 1], acc, wm, wn, lane, pl, sn);
+            mx::compute_held(sm.st[s & 1], acc, wm, wn, lane, pl, sn, sn * mx::BK);
             mx::wait_vmcnt<mx::kIssued8>();            // slab s + 1 has landed
             __syncthreads();
         }
@@ -416,7 +469,7 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
                 }
         }
         return;
-    } else {
+    } else if constexpr (std::is_same_v<Finish, StoreC>) {
     // The MFMAs take the B fragment first, so block (i, jj) holds the
     // transposed 16 x 16 product: lane l has output row l % 16 and columns
     // 4 * (l / 16) + v, four consecutive columns stored at once.  A tile
@@ -461,11 +514,70 @@ __global__ __launch_bounds__(mx::NT) void mxfp4_gemm_big_kernel(Mx8GemmParams p)
     mx_gemm_big<true, BF16_OUT>(p, smem_raw);
 }
 
+// The product as dH of a gated feed-forward block: the accumulators never
+// leave the registers; the 8-bit checkpoints of the tile come through LDS, and
+// each lane turns its own outputs into dgate and dup.
+template <int ACT, bool BF16_OUT>
+struct GatedBwd {
+    const GatedBwdParams &p;
+    __device__ const uint8_t *tile0() const { return p.g_codes; }
+    __device__ const uint8_t *tile1() const { return p.u_codes; }
+
+    // g and u: the tile's codes in LDS (byte_tile_plan), once the copies have landed
+    __device__ __forceinline__ void operator()(const uint8_t *g, const uint8_t *u, const f32x4 (&acc)[8][8],
+                                               int64_t m0, int64_t n0, int wm, int wn, int lane) const {
+        const int64_t M = p.mm.M, N = p.mm.N, nb = N / 32, b0 = (n0 + wn * 128) / 32;
+        const bool full = m0 + mx::BM <= M && n0 + mx::BN <= N;
+        // the block scales of the lane's row in each row block: four bytes
+        uint32_t gs[8], us[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t m = min(m0 + wm * 128 + i * 16 + (lane & 15), M - 1);
+            if (full) {
+                __builtin_memcpy(&gs[i], p.g_scales + m * nb + b0, 4);
+                __builtin_memcpy(&us[i], p.u_scales + m * nb + b0, 4);
+            } else {
+                gs[i] = us[i] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int64_t at = m * nb + min(b0 + b, nb - 1);
+                    gs[i] |= (uint32_t)p.g_scales[at] << (8 * b);
+                    us[i] |= (uint32_t)p.u_scales[at] << (8 * b);
+                }
+            }
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        const int64_t nl = n0 + wn * 128 + 4 * (lane >> 4);
+        const uint8_t *const gp = g + wn * (mx::BM * mx::BK), *const up = u + wn * (mx::BM * mx::BK);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = wm * 128 + i * 16 + (lane & 15);
+            const int64_t m = m0 + r;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+                const int at = r * mx::BK + 16 * mx::swz(r, jj) + 4 * (lane >> 4);
+                const uint32_t gw = *reinterpret_cast<const uint32_t *>(gp + at);
+                const uint32_t uw = *reinterpret_cast<const uint32_t *>(up + at);
+                if (full || (m < M && nl + jj * 16 < N))
+                    gated_bwd4<ACT, BF16_OUT>(p, m, nl + jj * 16, acc[i][jj], gw,
+                                              (gs[i] >> (8 * (jj >> 1))) & 0xFFu, uw,
+                                              (us[i] >> (8 * (jj >> 1))) & 0xFFu);
+            }
+        }
+    }
+};
+
+template <int ACT, bool BF16_OUT>
+__global__ __launch_bounds__(mx::NT) void mxfp8_gated_bwd_big_kernel(GatedBwdParams p) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    mx_gemm_big<false, BF16_OUT>(p.mm, smem_raw, GatedBwd<ACT, BF16_OUT>{p});
+}
+
 // The kernel's dynamic LDS limit is raised once per kernel (thread-safe
 // static initialisation).
-template <auto Kernel>
-static void launch_big(size_t shm, const Mx8GemmParams &p, hipStream_t s) {
-    const int64_t T = ((p.M + mx::BM - 1) / mx::BM) * ((p.N + mx::BN - 1) / mx::BN);
+template <auto Kernel, typename Params>
+static void launch_big(size_t shm, const Params &p, int64_t T, hipStream_t s) {
     static const bool attr_set = [shm] {
         (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
@@ -475,17 +587,34 @@ static void launch_big(size_t shm, const Mx8GemmParams &p, hipStream_t s) {
     hipLaunchKernelGGL(Kernel, dim3((unsigned)T), dim3(mx::NT), shm, s, p);
 }
 
+static int64_t big_tiles(const Mx8GemmParams &p) {
+    return ((p.M + mx::BM - 1) / mx::BM) * ((p.N + mx::BN - 1) / mx::BN);
+}
+
+hipError_t launch_gated_bwd_big(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
+    const size_t shm = sizeof(mx::Smem<false>);
+    const int64_t T = big_tiles(p.mm);
+    if (act == kActGelu) {
+        if (bf16_out) launch_big<mxfp8_gated_bwd_big_kernel<kActGelu, true>>(shm, p, T, s);
+        else launch_big<mxfp8_gated_bwd_big_kernel<kActGelu, false>>(shm, p, T, s);
+    } else {
+        if (bf16_out) launch_big<mxfp8_gated_bwd_big_kernel<kActSilu, true>>(shm, p, T, s);
+        else launch_big<mxfp8_gated_bwd_big_kernel<kActSilu, false>>(shm, p, T, s);
+    }
+    return hipGetLastError();
+}
+
 hipError_t launch_mxfp8_gemm_big(const Mx8GemmParams &p, bool bf16_out, hipStream_t s) {
     const size_t shm = sizeof(mx::Smem<false>);
-    if (bf16_out) launch_big<mxfp8_gemm_big_kernel<true>>(shm, p, s);
-    else launch_big<mxfp8_gemm_big_kernel<false>>(shm, p, s);
+    if (bf16_out) launch_big<mxfp8_gemm_big_kernel<true>>(shm, p, big_tiles(p), s);
+    else launch_big<mxfp8_gemm_big_kernel<false>>(shm, p, big_tiles(p), s);
     return hipGetLastError();
 }
 
 hipError_t launch_mxfp4_gemm(const Mx8GemmParams &p, bool bf16_out, hipStream_t s) {
     const size_t shm = sizeof(mx::Smem<true>);
-    if (bf16_out) launch_big<mxfp4_gemm_big_kernel<true>>(shm, p, s);
-    else launch_big<mxfp4_gemm_big_kernel<false>>(shm, p, s);
+    if (bf16_out) launch_big<mxfp4_gemm_big_kernel<true>>(shm, p, big_tiles(p), s);
+    else launch_big<mxfp4_gemm_big_kernel<false>>(shm, p, big_tiles(p), s);
     return hipGetLastError();
 }
 

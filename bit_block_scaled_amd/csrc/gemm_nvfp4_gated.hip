@@ -49,7 +49,7 @@ __device__ __forceinline__ void gated_epilogue(uint8_t *stage, uint8_t *stage2, 
             for (int q = 0; q < 4; ++q) {
                 float h[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = gate_act<ACT>(g[4 * q + e]) * u[4 * q + e];
+                for (int e = 0; e < 4; ++e) h[e] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
                 store4<BF16_OUT>(row, j * 32 + 8 * q + 4 * half, h[0], h[1], h[2], h[3]);
             }
         }

@@ -54,7 +54,7 @@ __device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n
     float y = SC == kRows32 ? v[0] : v[0] * p.w.s_dec[0];
     if constexpr (NM == 2) {
         const float u = SC == kRows32 ? v[1] : v[1] * p.u.s_dec[0];
-        y = (p.act == kActSilu ? gate_act<kActSilu>(y) : gate_act<kActGelu>(y)) * u;
+        y = (p.act == kActSilu ? gate_act<kActSilu, false>(y) : gate_act<kActGelu, false>(y)) * u;
     }
     if (p.bf16_out) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(y, y);
     else static_cast<float *>(p.y)[t * p.ldy + n] = y;

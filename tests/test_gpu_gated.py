@@ -350,6 +350,35 @@ def test_gated_bwd(bbs, M, F, K, act, bf16, pad):
     check(buf, M, 2 * F, bf16, np.concatenate([dh * u * sl, dh * a], 1), np.concatenate([E_g, E_u], 1), "dg, du")
 
 
+@pytest.mark.parametrize("K", [128, 160])
+def test_gated_bwd_scale_bytes(bbs, K):
+    """Checkpoint blocks at the smallest and large scales, every code among them, beside ordinary ones."""
+    announce(f"gated bwd scale bytes K={K}")
+    M, F = 32, 96
+    rng = np.random.default_rng(9)
+    oy = O.mxfp8_quantize(synth.normal(M, K, 75, 1.0), mode=O.RTN)
+    ow = O.mxfp8_quantize(synth.normal(F, K, 76, 1.0), mode=O.RTN)
+    codes = rng.integers(0, 256, (2, M, F)).astype(np.uint8)
+    codes[(codes & 0x7F) == 0x7F] ^= 1                                   # no NaN
+    sc = np.array([[0, 1, 30, 110, 118, 121], [121, 140, 118, 0, 127, 60]], np.uint8)
+    sc = np.stack([rng.choice(s, (M, F // 32)) for s in sc])
+    og, ou = (O.MXFP8(codes[i], sc[i], M, F) for i in (0, 1))
+    d = torch.empty((2, M, F), dtype=torch.float32, device=dev())
+    dh, Ed = product_mx8(oy.dequant_f64(), ow.dequant_f64())
+    g, u = og.dequant_f64(), ou.dequant_f64()
+    for act in ("silu", "gelu"):
+        bbs.mxfp8_gemm_gated_bwd(upload_mxfp8(oy, bbs), upload_mxfp8(ow, bbs), upload_mxfp8(og, bbs),
+                                 upload_mxfp8(ou, bbs), d[0], d[1], 0, act=int(act == "gelu"))
+        torch.cuda.synchronize()
+        a, sl = act64(act, g), act_slope64(act, g)
+        tiny = 2.0 ** -120 * (1 + np.abs(dh)) * (1 + np.abs(u))
+        E_g = np.abs(u) * ((np.abs(dh) + Ed) * slope_error(act, g) + np.abs(sl) * Ed) + 3 * ULP * np.abs(dh * u * sl)
+        E_u = (np.abs(dh) + Ed) * act_error(act, g) + np.abs(a) * Ed + 2 * ULP * np.abs(dh * a)
+        got = host(d).astype(np.float64)
+        assert np.all(np.abs(got[0] - dh * u * sl) <= E_g + tiny), act
+        assert np.all(np.abs(got[1] - dh * a) <= E_u + tiny), act
+
+
 def test_bwd_is_the_gradient_of_the_forward_pass(bbs):
     """Central differences of sum(dH * h) through the forward kernel's own
     formula at the checkpointed values match dG and dU."""
