@@ -1,245 +1,417 @@
-// Gated feed-forward operators, kernels for any K the formats allow (gfx950).
+// Gated feed-forward operators, small-tile kernels for any K the formats
+// allow (gfx950), and the choice between them and the large-tile kernels.
 //
 //   forward   g = A Wg^T, u = A Wu^T (NVFP4 x NVFP4), h = act(g) * u, and
 //             optionally MXFP8 checkpoints of the FP32 g and u
 //   backward  dh = dY W (MXFP8 x MXFP8), dg = dh * u * act'(g),
 //             du = dh * act(g), with g and u read back from the checkpoints
 //
-// Both products of the forward pass share one tile: its B side interleaves
-// 32-column blocks of the gate and up weights, so the lane that holds g of an
-// output also holds u, and h needs no exchange.  The activation works on the
-// FP32 sums and each output is rounded once.
+// A workgroup of four waves (2 x 2) walks K in slabs of 128 through a ring of
+// LDS stages filled by asynchronous copies, as the large-tile kernels do, but
+// with tiles small enough for two or more workgroups a CU: one's arithmetic
+// covers another's waits, and a problem of a few hundred rows still reaches
+// every CU.
 //
-// These kernels take 128-row tiles and stage through registers; the large
-// tile kernels beside the plain GEMMs serve K % 128 == 0.
-#include "bbs_device.hpp"
+// K's last slab may be partial and rows may start at any multiple of 8 bytes
+// (codes) or at any byte (scales).  Codes are copied in 16-byte pieces from
+// where they are; what a piece reads past K belongs to the next row and is
+// cancelled by a zero scale, or overwritten by zeros where a code could be NaN.
+// Scales are copied as the aligned words that contain them and shifted into
+// place when they are read; the shift is the same in every slab.  No copy
+// leaves the operand's own bytes but for the rest of the words at its ends.
+#include "gemm_nvfp4_tiles.hpp"
 #include "gated_epilogue.hpp"
 
 namespace bbs {
 
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr int kBM = 128, kBF = 64, kBK = 64, kThreads = 256;
-constexpr int kStride = kBK / 2 + 4;           // padded row of packed codes
+constexpr int kThreads = 256;
 
-struct FwdSmem {
-    uint8_t a[kBM * kStride];
-    uint8_t b[2 * kBF * kStride];
-    uint8_t as[kBM * 4], bs[2 * kBF * 4];
-};
-
-// Eight E2M1 codes times one E4M3 scale in FP16 (exact: at most 6
-// significant bits in [2^-10, 2688]).
-__device__ __forceinline__ f16x8 expand8(uint32_t w, uint32_t scale_byte) {
-    const f16x2 s2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(scale_byte, 1.0f, false);
-    const f16x2 s = {s2[0], s2[0]};
-    const f16x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s;
-    const f16x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s;
-    const f16x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s;
-    const f16x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s;
-    return f16x8{v0[0], v0[1], v1[0], v1[1], v2[0], v2[1], v3[0], v3[1]};
+// The aligned word at or before p, and the last one an array [p, p + bytes) touches.
+__device__ __forceinline__ const uint8_t *word_of(const uint8_t *p) {
+    return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
 }
+__device__ __forceinline__ const uint8_t *lesser(const uint8_t *a, const uint8_t *b) { return a < b ? a : b; }
+
+// Adds the sums of groups 1 .. G - 1 to group 0's, in that order.
+template <int G, int NV>
+__device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, int lane, float (&v)[NV]) {
+    if (G == 1) return;
+    __syncthreads();                               // the rings are free
+    float *const part = reinterpret_cast<float *>(smem) + (wave * NV) * 64 + lane;
+    if (grp) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) part[((grp - 1) * 4 * NV + i) * 64] = v[i];
+    }
+    __syncthreads();
+    if (!grp) {
+#pragma unroll
+        for (int g = 1; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] += part[((g - 1) * 4 * NV + i) * 64];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Forward: TM rows by 64 columns of both products.
+// ---------------------------------------------------------------------------
+constexpr int kBF = 64;
+
+template <int TM>
+struct FwdStage {
+    uint8_t a[TM * 64];              // 64 code bytes a row and slab, swizzled as big::Stage
+    uint8_t b[2 * kBF * 64];
+    uint32_t sc[3][TM + 2 * kBF];    // the words that hold a row's 8 scale bytes (A rows, then B rows)
+};
 
 // The tile's B row r holds weight row n0 + 32 (r / 64) + r % 32, of the gate
 // matrix where r / 32 is even and of the up matrix where it is odd.
-__device__ __forceinline__ int64_t b_column(int r) { return 32 * (r >> 6) + (r & 31); }
+__device__ __forceinline__ int b_column(int r) { return 32 * (r >> 6) + (r & 31); }
 
-template <int ACT, bool BF16_OUT, bool CKPT>
-__global__ __launch_bounds__(kThreads) void gated_gemm_kernel(GatedParams p) {
-    __shared__ FwdSmem sm;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+template <int TM, int NS, int G, int ACT, bool BF16_OUT>
+__global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p) {
+    constexpr int RA = TM / 64;                    // 32-row blocks of a wave
+    constexpr int kIssued = RA + 2 + 3;            // copies one wave issues a slab
+    constexpr int AHEAD = NS - 1;                  // slabs in flight beyond the one consumed
+    extern __shared__ __align__(16) uint8_t smem[];
+    // four waves a group; group g of G takes slabs g, g + G, ... in its own ring
+    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    FwdStage<TM> *const st = reinterpret_cast<FwdStage<TM> *>(smem) + grp * NS;
+    const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t tm = (p.M + kBM - 1) / kBM;
-    const int64_t m0 = blockIdx.x % tm * kBM, n0 = blockIdx.x / tm * kBF;
+    const int64_t tm = (p.M + TM - 1) / TM;
+    const int64_t m0 = blockIdx.x % tm * TM, n0 = blockIdx.x / tm * kBF;
     const int64_t kb = p.K / 2, ks = p.K / 16;
-    // staging: thread t copies 32 codes (16 bytes) of row t / 2 of each side
-    const int row = t >> 1, half = t & 1;
-    const int64_t am = m0 + row, bn = n0 + b_column(row);
-    const Fp4View &W = ((row >> 5) & 1) ? p.u : p.b;
-    const bool a_ok = am < p.M, b_ok = bn < p.N;
-    // scales: threads 0-127 the A side's rows, the others the B side's
-    const int sr = t & 127;
-    const bool sb = t >= 128;
-    const Fp4View &S = sb ? (((sr >> 5) & 1) ? p.u : p.b) : p.a;
-    const int64_t srow = sb ? n0 + b_column(sr) : m0 + sr;
-    const bool s_ok = srow < (sb ? p.N : p.M);
-    const uint8_t *sp = S.scales + (S.tile2d ? srow / 16 : srow) * ks;
+    const int64_t nslab = (p.K + 127) / 128;
+    const int tail = (int)(p.K % 128);             // K values of a partial last slab, 0: none
 
-    f32x16 acc[2][2];
+    // copy sources (rows past the end are clamped: they feed nothing that is written)
+    const uint8_t *asrc[RA], *bsrc[2], *aend, *bend[2];
+    const int pos = big::swz(lane >> 2, lane & 3);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int q = 0; q < RA; ++q) {
+        const int64_t m = min(m0 + (wave * RA + q) * 16 + (lane >> 2), p.M - 1);
+        asrc[q] = p.a.codes + m * kb + 16 * pos;
+    }
+    aend = p.a.codes + p.a.rows * kb - 16;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int r = (wave * 2 + q) * 16 + (lane >> 2);
+        const Fp4View &W = ((r >> 5) & 1) ? p.u : p.b;
+        bsrc[q] = W.codes + min(n0 + b_column(r), p.N - 1) * kb + 16 * pos;
+        bend[q] = W.codes + p.N * kb - 16;
+    }
+    // scales: wave w copies the words of rows 64 w .. 64 w + 63 (the waves past
+    // the last row repeat the last 64)
+    auto scale_row = [&](int r) -> const uint8_t * {
+        if (r < TM) {
+            const int64_t m = min(m0 + r, p.M - 1);
+            return p.a.scales + (p.a.tile2d ? m / 16 : m) * ks;
+        }
+        const Fp4View &W = (((r - TM) >> 5) & 1) ? p.u : p.b;
+        const int64_t n = min(n0 + b_column(r - TM), p.N - 1);
+        return W.scales + (W.tile2d ? n / 16 : n) * ks;
+    };
+    const int sgroup = min(wave, (TM + 2 * kBF) / 64 - 1) * 64;
+    const uint8_t *ssrc, *slast;
+    {
+        const int r = sgroup + lane;
+        const Fp4View &W = r < TM ? p.a : (((r - TM) >> 5) & 1) ? p.u : p.b;
+        const int64_t rows = r < TM ? p.a.rows : p.N;
+        ssrc = word_of(scale_row(r));
+        slast = word_of(W.scales + (W.tile2d ? rows / 16 : rows) * ks - 1);
+    }
+    auto issue = [&](int64_t s, int stage) {
+        FwdStage<TM> &d = st[stage];
+        const int64_t at = s * 64;
+        const bool partial = tail && s == nslab - 1;
+#pragma unroll
+        for (int q = 0; q < RA; ++q)
+            copy_lds16(partial ? lesser(asrc[q] + at, aend) : asrc[q] + at, d.a + (wave * RA + q) * 1024);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            copy_lds16(partial ? lesser(bsrc[q] + at, bend[q]) : bsrc[q] + at, d.b + (wave * 2 + q) * 1024);
+#pragma unroll
+        for (int w = 0; w < 3; ++w) copy_lds4(lesser(ssrc + s * 8 + 4 * w, slast), &d.sc[w][sgroup]);
+    };
+
+    // the lane's fragment rows and the byte shift of their scales
+    const int h = lane >> 5, rl = lane & 31;
+    int sha[RA], shb[2];
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
+        sha[i] = (int)(reinterpret_cast<uintptr_t>(scale_row(wm * (TM / 2) + i * 32 + rl)) & 3);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        shb[j] = (int)(reinterpret_cast<uintptr_t>(scale_row(TM + wn * 64 + j * 32 + rl)) & 3);
+
+    f32x16 acc[RA][2];
+#pragma unroll
+    for (int i = 0; i < RA; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{0};
 
-    for (int64_t k0 = 0; k0 < p.K; k0 += kBK) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int64_t k = k0 + half * 32 + q * 16;
-            uint2 va = make_uint2(0, 0), vb = make_uint2(0, 0);
-            if (a_ok && k < p.K) va = *reinterpret_cast<const uint2 *>(p.a.codes + am * kb + k / 2);
-            if (b_ok && k < p.K) vb = *reinterpret_cast<const uint2 *>(W.codes + bn * kb + k / 2);
-            uint32_t *da = reinterpret_cast<uint32_t *>(sm.a + row * kStride + half * 16 + q * 8);
-            uint32_t *db = reinterpret_cast<uint32_t *>(sm.b + row * kStride + half * 16 + q * 8);
-            da[0] = va.x;
-            da[1] = va.y;
-            db[0] = vb.x;
-            db[1] = vb.y;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t k = k0 / 16 + j;
-            (sb ? sm.bs : sm.as)[sr * 4 + j] = (s_ok && k < ks) ? sp[k] : (uint8_t)0;
-        }
+    const int64_t own = (nslab - grp + G - 1) / G;       // the group's slabs
+    for (int k = 0; k < AHEAD; ++k)
+        if (k < own) issue(k * G + grp, k);
+    int rd = 0, wr = AHEAD;                              // stages of its slab it and of slab it + AHEAD
+    for (int64_t it = 0; it < (nslab + G - 1) / G; ++it) {
+        if (it + AHEAD <= own) big::wait_vmcnt<(AHEAD - 1) * kIssued>();    // slab it has landed
+        else big::wait_vmcnt<0>();
         __syncthreads();
+        const int64_t s = it * G + grp;
+        if (it + AHEAD < own) issue(s + AHEAD * G, wr);  // into the stage read before this barrier
+        FwdStage<TM> &d = st[rd];
+        rd = rd + 1 == NS ? 0 : rd + 1;
+        wr = wr + 1 == NS ? 0 : wr + 1;
+        uint32_t keep[2] = {~0u, ~0u};                   // scale bytes of blocks inside K
+        const bool last = tail && s == nslab - 1;
+        if (last) {
+            const int nb = tail / 16;
+            keep[0] = nb >= 4 ? ~0u : (1u << (8 * nb)) - 1;
+            keep[1] = nb <= 4 ? 0u : nb >= 8 ? ~0u : (1u << (8 * (nb - 4))) - 1;
+        }
+        if (tail % 32 && it == (nslab - 1) / G) {
+            // an operand's very last row ends in half a piece, which was copied
+            // from 8 bytes earlier: move it into place
+            const int c = tail / 32;
+            const int64_t col = p.N - 1 - n0;
+            const int64_t r = t == 0 ? p.a.rows - 1 - m0 : 64 * (col >> 5) + 32 * (t - 1) + (col & 31);
+            if (last && (t == 0 ? r < TM : t <= 2 && col < kBF)) {
+                uint8_t *piece = (t == 0 ? d.a : d.b) + r * 64 + 16 * big::swz((int)r, c);
+                *reinterpret_cast<uint2 *>(piece) = *reinterpret_cast<const uint2 *>(piece + 8);
+            }
+            __syncthreads();
+        }
+        if (G > 1 && s >= nslab) continue;
+        uint32_t sa[RA][2], sb[2][2];
+        auto scales = [&](uint32_t (&o)[2], int row, int shift) {
+            const uint32_t w0 = d.sc[0][row], w1 = d.sc[1][row], w2 = d.sc[2][row];
+            o[0] = __builtin_amdgcn_alignbyte(w1, w0, shift) & keep[0];
+            o[1] = __builtin_amdgcn_alignbyte(w2, w1, shift) & keep[1];
+        };
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int h = lane >> 5, rl = lane & 31;
-            f16x8 af[2], bf[2];
+        for (int i = 0; i < RA; ++i) scales(sa[i], wm * (TM / 2) + i * 32 + rl, sha[i]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = wm * 64 + i * 32 + rl;
-                af[i] = expand8(*reinterpret_cast<const uint32_t *>(sm.a + r * kStride + kk * 8 + h * 4),
-                                sm.as[r * 4 + kk]);
+        for (int j = 0; j < 2; ++j) scales(sb[j], TM + wn * 64 + j * 32 + rl, shb[j]);
+        uint4 ca[2][RA], cb[2][2];
+        f16x2 pa[2][RA], pb[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int i = 0; i < RA; ++i) {
+                const int r = wm * (TM / 2) + i * 32 + rl;
+                ca[c][i] = *reinterpret_cast<const uint4 *>(d.a + r * 64 + 16 * big::swz(r, 2 * c + h));
+                pa[c][i] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sa[i][c] >> (16 * h), 1.0f, false);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int r = wn * 64 + j * 32 + rl;
-                bf[j] = expand8(*reinterpret_cast<const uint32_t *>(sm.b + r * kStride + kk * 8 + h * 4),
-                                sm.bs[r * 4 + kk]);
+                cb[c][j] = *reinterpret_cast<const uint4 *>(d.b + r * 64 + 16 * big::swz(r, 2 * c + h));
+                pb[c][j] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb[j][c] >> (16 * h), 1.0f, false);
             }
+        }
+        // eight MFMA steps; the operands of step k + 1 are expanded between the
+        // MFMAs of step k
+        f16x8 af[2][RA], bf[2][2];
+        auto expand = [&](int k) __attribute__((always_inline)) {
+            const int c = k >> 2, w = k & 3;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < RA; ++i) af[k & 1][i] = big::expand8_f16(big::word(ca[c][i], w), pa[c][i][w >> 1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) bf[k & 1][j] = big::expand8_f16(big::word(cb[c][j], w), pb[c][j][w >> 1]);
+        };
+        expand(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k < 7) expand(k + 1);
+#pragma unroll
+            for (int i = 0; i < RA; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[j], af[i], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[k & 1][j], af[k & 1][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+            for (int m = 0; m < 2 * RA; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, (RA + 2) * 8 / (2 * RA), 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
     }
 
+    join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[RA * 32]>(acc));
+    if (grp) return;
     const float sg = p.b.s_dec[0], su = p.u.s_dec[0];
-    const int64_t n = n0 + wn * 32 + 4 * (lane >> 5);      // the lane's first column
+    const int64_t nb = n0 + wn * 32, n = nb + 4 * h;       // the block's and the lane's first column
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t m = m0 + wm * 64 + i * 32 + (lane & 31);
-        const int64_t ms = m < p.M ? m : p.M - 1;
-        const float sa = p.a.s_dec[p.a.sdec_rows ? ms : 0];
+    for (int i = 0; i < RA; ++i) {
+        const int64_t m = m0 + wm * (TM / 2) + i * 32 + rl;
+        const float sa = p.a.s_dec[p.a.sdec_rows ? (m < p.M ? m : p.M - 1) : 0];
         f32x16 g = acc[i][0], u = acc[i][1];
         scale16(g, sa * sg);
         scale16(u, sa * su);
-        if (CKPT) {
+        if (p.g_codes) {
             uint32_t w[4];
             const uint32_t bg = checkpoint16(g, w);
-            if (m < p.M) store_checkpoint(w, bg, p.g_codes, p.g_scales, p.N, m, n, lane);
+            store_checkpoint16(w, bg, p.g_codes, p.g_scales, p.N, m < p.M, m, nb, h);
             const uint32_t bu = checkpoint16(u, w);
-            if (m < p.M) store_checkpoint(w, bu, p.u_codes, p.u_scales, p.N, m, n, lane);
+            store_checkpoint16(w, bu, p.u_codes, p.u_scales, p.N, m < p.M, m, nb, h);
         }
         if (m >= p.M) continue;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (n + 8 * q >= p.N) continue;
-            store4<BF16_OUT>(p.h, m * p.ldh + n + 8 * q, gate_act<ACT, BF16_OUT>(g[4 * q]) * u[4 * q],
-                             gate_act<ACT, BF16_OUT>(g[4 * q + 1]) * u[4 * q + 1],
-                             gate_act<ACT, BF16_OUT>(g[4 * q + 2]) * u[4 * q + 2],
-                             gate_act<ACT, BF16_OUT>(g[4 * q + 3]) * u[4 * q + 3]);
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
+            store4<BF16_OUT>(p.h, m * p.ldh + n + 8 * q, y[0], y[1], y[2], y[3]);
         }
     }
 }
 
-// Backward, 128 x 128 tiles with a K slab of 128 (one MFMA deep); operand
-// layout of the scaled MFMA as in the plain MXFP8 GEMM: lane group g feeds
-// bytes [16g, 16g + 16) and [64 + 16g, 64 + 16g + 16) of its row and the
-// scale of the slab's 32-block g.
-constexpr int kMxBK = 128, kMxStride = kMxBK + 16;
-
-struct BwdSmem {
-    uint8_t a[128 * kMxStride];
-    uint8_t b[128 * kMxStride];
-    uint8_t as[128 * 4], bs[128 * 4];
+// ---------------------------------------------------------------------------
+// Backward: T x T tiles.  Operand layout of the scaled MFMA as in the plain
+// MXFP8 GEMM: lane group g feeds bytes [16g, 16g + 16) and [64 + 16g, 64 + 16g
+// + 16) of its row and the scale of the slab's 32-block g.
+// ---------------------------------------------------------------------------
+template <int T>
+struct BwdStage {
+    uint8_t a[T * 128];              // chunk c of row r at place c ^ ((r >> 1) & 7)
+    uint8_t b[T * 128];
+    uint32_t sc[2][2 * T];           // the words that hold a row's 4 scale bytes
 };
 
-template <int ACT, bool BF16_OUT>
-__global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedBwdParams p) {
-    __shared__ BwdSmem sm;
+__device__ __forceinline__ int swz8(int row, int chunk) { return chunk ^ ((row >> 1) & 7); }
+
+template <int T, int NS, int G, int ACT, bool BF16_OUT>
+__global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams p) {
+    constexpr int AHEAD = NS - 1;
+    constexpr int Q = T / 32;                          // 1 KB copies of a wave and operand; MFMA blocks a side
+    constexpr int kIssued = 2 * Q + 2;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    BwdStage<T> *const st = reinterpret_cast<BwdStage<T> *>(smem) + grp * NS;
     const Mx8GemmParams &mm = p.mm;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t tm = (mm.M + 127) / 128;
-    const int64_t m0 = blockIdx.x % tm * 128, n0 = blockIdx.x / tm * 128;
-    const int64_t nkb = mm.K / 32;
+    const int64_t tm = (mm.M + T - 1) / T;
+    const int64_t m0 = blockIdx.x % tm * T, n0 = blockIdx.x / tm * T;
+    const int64_t nkb = mm.K / 32, nslab = (mm.K + 127) / 128;
+    const int tail = (int)(mm.K % 128);
 
-    f32x4 acc[4][4];
+    const uint8_t *asrc[Q], *bsrc[Q];
+    const uint8_t *const aend = mm.a_codes + mm.M * mm.K - 16, *const bend = mm.b_codes + mm.N * mm.K - 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int q = 0; q < Q; ++q) {
+        const int row = (wave * Q + q) * 8 + (lane >> 3), c = swz8(row, lane & 7);
+        asrc[q] = mm.a_codes + min(m0 + row, mm.M - 1) * mm.K + 16 * c;
+        bsrc[q] = mm.b_codes + min(n0 + row, mm.N - 1) * mm.K + 16 * c;
+    }
+    auto scale_row = [&](int r) -> const uint8_t * {
+        return r < T ? mm.a_scales + min(m0 + r, mm.M - 1) * nkb : mm.b_scales + min(n0 + r - T, mm.N - 1) * nkb;
+    };
+    const int sgroup = min(wave, 2 * T / 64 - 1) * 64;
+    const uint8_t *const ssrc = word_of(scale_row(sgroup + lane));
+    const uint8_t *const slast = sgroup + lane < T ? word_of(mm.a_scales + mm.M * nkb - 1)
+                                                   : word_of(mm.b_scales + mm.N * nkb - 1);
+    auto issue = [&](int64_t s, int stage) {
+        BwdStage<T> &d = st[stage];
+        const int64_t at = s * 128;
+        const bool partial = tail && s == nslab - 1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0};
+        for (int q = 0; q < Q; ++q) {
+            copy_lds16(partial ? lesser(asrc[q] + at, aend) : asrc[q] + at, d.a + (wave * Q + q) * 1024);
+            copy_lds16(partial ? lesser(bsrc[q] + at, bend) : bsrc[q] + at, d.b + (wave * Q + q) * 1024);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) copy_lds4(lesser(ssrc + s * 4 + 4 * w, slast), &d.sc[w][sgroup]);
+    };
 
-    for (int64_t k0 = 0; k0 < mm.K; k0 += kMxBK) {
+    const int kg = lane >> 4, rl = lane & 15;
+    int sha[Q], shb[Q];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int idx = q * kThreads + t;
-            const int row = idx >> 3, seg = idx & 7;
-            const int64_t k = k0 + seg * 16;
-            uint4 va = make_uint4(0, 0, 0, 0), vb = make_uint4(0, 0, 0, 0);
-            if (m0 + row < mm.M && k < mm.K)
-                va = *reinterpret_cast<const uint4 *>(mm.a_codes + (m0 + row) * mm.K + k);
-            if (n0 + row < mm.N && k < mm.K)
-                vb = *reinterpret_cast<const uint4 *>(mm.b_codes + (n0 + row) * mm.K + k);
-            *reinterpret_cast<uint4 *>(sm.a + row * kMxStride + seg * 16) = va;
-            *reinterpret_cast<uint4 *>(sm.b + row * kMxStride + seg * 16) = vb;
-        }
-        {
-            const int row = t & 127;
-            const bool isb = t >= 128;
-            const int64_t gr = (isb ? n0 : m0) + row;
-            const uint8_t *sc = isb ? mm.b_scales : mm.a_scales;
-            uint8_t *dst = isb ? sm.bs : sm.as;
+    for (int i = 0; i < Q; ++i) {
+        sha[i] = (int)(reinterpret_cast<uintptr_t>(scale_row(wm * (T / 2) + i * 16 + rl)) & 3);
+        shb[i] = (int)(reinterpret_cast<uintptr_t>(scale_row(T + wn * (T / 2) + i * 16 + rl)) & 3);
+    }
+    f32x4 acc[Q][Q];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t kb = k0 / 32 + j;
-                dst[row * 4 + j] = (gr < (isb ? mm.N : mm.M) && kb < nkb) ? sc[gr * nkb + kb] : (uint8_t)0;
-            }
-        }
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+        for (int j = 0; j < Q; ++j) acc[i][j] = f32x4{0};
+
+    const int64_t own = (nslab - grp + G - 1) / G;       // the group's slabs
+    for (int k = 0; k < AHEAD; ++k)
+        if (k < own) issue(k * G + grp, k);
+    int rd = 0, wr = AHEAD;                              // stages of its slab it and of slab it + AHEAD
+    for (int64_t it = 0; it < (nslab + G - 1) / G; ++it) {
+        if (it + AHEAD <= own) big::wait_vmcnt<(AHEAD - 1) * kIssued>();    // slab it has landed
+        else big::wait_vmcnt<0>();
         __syncthreads();
-        const int kg = lane >> 4;
-        i32x8 af[4], bf[4];
-        int as_[4], bs_[4];
-        auto fragment = [&](const uint8_t *row) {
-            const uint4 x0 = *reinterpret_cast<const uint4 *>(row + 16 * kg);
-            const uint4 x1 = *reinterpret_cast<const uint4 *>(row + 64 + 16 * kg);
+        const int64_t s = it * G + grp;
+        if (it + AHEAD < own) issue(s + AHEAD * G, wr);  // into the stage read before this barrier
+        BwdStage<T> &d = st[rd];
+        rd = rd + 1 == NS ? 0 : rd + 1;
+        wr = wr + 1 == NS ? 0 : wr + 1;
+        uint32_t keep = ~0u;
+        if (tail && it == (nslab - 1) / G) {
+            if (s == nslab - 1) {
+                // chunks past K hold other rows' codes: zeros, with scale byte 0
+                keep = (1u << (8 * (tail / 32))) - 1;
+                const int first = tail / 16, n = 8 - first;
+                for (int e = t; e < 2 * T * n; e += kThreads) {
+                    const int r = e / n % T, c = first + e % n;
+                    *reinterpret_cast<uint4 *>((e < T * n ? d.a : d.b) + r * 128 + 16 * swz8(r, c)) =
+                        make_uint4(0, 0, 0, 0);
+                }
+            }
+            __syncthreads();
+        }
+        if (G > 1 && s >= nslab) continue;
+        i32x8 af[Q], bf[Q];
+        int sa[Q], sb[Q];
+        auto fragment = [&](const uint8_t *side, int r) {
+            const uint4 x0 = *reinterpret_cast<const uint4 *>(side + r * 128 + 16 * swz8(r, kg));
+            const uint4 x1 = *reinterpret_cast<const uint4 *>(side + r * 128 + 16 * swz8(r, 4 + kg));
             return i32x8{(int)x0.x, (int)x0.y, (int)x0.z, (int)x0.w,
                          (int)x1.x, (int)x1.y, (int)x1.z, (int)x1.w};
         };
+        auto scale = [&](int row, int shift) {
+            const uint32_t w = __builtin_amdgcn_alignbyte(d.sc[1][row], d.sc[0][row], shift) & keep;
+            return (int)((w >> (8 * kg)) & 0xFFu);
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ra = wm * 64 + i * 16 + (lane & 15), rb = wn * 64 + i * 16 + (lane & 15);
-            af[i] = fragment(sm.a + ra * kMxStride);
-            bf[i] = fragment(sm.b + rb * kMxStride);
-            as_[i] = sm.as[ra * 4 + kg];
-            bs_[i] = sm.bs[rb * 4 + kg];
+        for (int i = 0; i < Q; ++i) {
+            const int ra = wm * (T / 2) + i * 16 + rl, rb = wn * (T / 2) + i * 16 + rl;
+            af[i] = fragment(d.a, ra);
+            bf[i] = fragment(d.b, rb);
+            sa[i] = scale(ra, sha[i]);
+            sb[i] = scale(T + rb, shb[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < Q; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    bf[j], af[i], acc[i][j], 0, 0, 0, bs_[j], 0, as_[i]);
-        __syncthreads();
+            for (int j = 0; j < Q; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(bf[j], af[i], acc[i][j], 0, 0, 0,
+                                                                             sb[j], 0, sa[i]);
     }
 
+    join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[Q * Q * 4]>(acc));
+    if (grp) return;
     // the B fragment goes first, so lane l holds row l % 16 and four
     // consecutive columns from 4 (l / 16) of every block
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + wm * 64 + i * 16 + (lane & 15);
+    for (int i = 0; i < Q; ++i) {
+        const int64_t m = m0 + wm * (T / 2) + i * 16 + rl;
         if (m >= mm.M) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + wn * 64 + j * 16 + 4 * (lane >> 4);
+        for (int j = 0; j < Q; ++j) {
+            const int64_t n = n0 + wn * (T / 2) + j * 16 + 4 * kg;
             if (n >= mm.N) continue;
             const int64_t at = m * mm.N + n, bl = m * (mm.N / 32) + n / 32;
             gated_bwd4<ACT, BF16_OUT>(p, m, n, acc[i][j], *reinterpret_cast<const uint32_t *>(p.g_codes + at),
@@ -249,45 +421,84 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_kernel(GatedBwdParams p) {
     }
 }
 
-template <int ACT, bool BF16_OUT>
-hipError_t fwd(const GatedParams &p, hipStream_t s) {
-    const int64_t tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBF - 1) / kBF);
+// Launch with dynamic LDS; the kernel's limit is raised once per kernel.
+template <auto Kernel, typename Params>
+hipError_t launch(int64_t tiles, int threads, size_t shm, const Params &p, hipStream_t s) {
     if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)tiles);
-    if (p.g_codes)
-        hipLaunchKernelGGL((gated_gemm_kernel<ACT, BF16_OUT, true>), grid, dim3(kThreads), 0, s, p);
-    else
-        hipLaunchKernelGGL((gated_gemm_kernel<ACT, BF16_OUT, false>), grid, dim3(kThreads), 0, s, p);
+    static const bool attr_set = [shm] {
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
+                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
+        return true;
+    }();
+    (void)attr_set;
+    hipLaunchKernelGGL(Kernel, dim3((unsigned)tiles), dim3((unsigned)threads), shm, s, p);
     return hipGetLastError();
 }
 
-template <int ACT, bool BF16_OUT>
-hipError_t bwd(const GatedBwdParams &p, hipStream_t s) {
-    const int64_t tiles = ((p.mm.M + 127) / 128) * ((p.mm.N + 127) / 128);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)tiles);
-    hipLaunchKernelGGL((gated_bwd_kernel<ACT, BF16_OUT>), grid, dim3(kThreads), 0, s, p);
-    return hipGetLastError();
+int64_t tiles_of(int64_t M, int64_t N, int tm, int tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); }
+
+template <int TM, int NS, int G>
+hipError_t fwd(const GatedParams &p, int act, bool bf16_out, hipStream_t s) {
+    const int64_t tiles = tiles_of(p.M, p.N, TM, kBF);
+    constexpr size_t shm = G * NS * sizeof(FwdStage<TM>);
+    if (act == kActGelu)
+        return bf16_out ? launch<gated_gemm_kernel<TM, NS, G, kActGelu, true>>(tiles, kThreads * G, shm, p, s)
+                        : launch<gated_gemm_kernel<TM, NS, G, kActGelu, false>>(tiles, kThreads * G, shm, p, s);
+    return bf16_out ? launch<gated_gemm_kernel<TM, NS, G, kActSilu, true>>(tiles, kThreads * G, shm, p, s)
+                    : launch<gated_gemm_kernel<TM, NS, G, kActSilu, false>>(tiles, kThreads * G, shm, p, s);
+}
+
+template <int T, int NS, int G>
+hipError_t bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
+    const int64_t tiles = tiles_of(p.mm.M, p.mm.N, T, T);
+    constexpr size_t shm = G * NS * sizeof(BwdStage<T>);
+    if (act == kActGelu)
+        return bf16_out ? launch<gated_bwd_kernel<T, NS, G, kActGelu, true>>(tiles, kThreads * G, shm, p, s)
+                        : launch<gated_bwd_kernel<T, NS, G, kActGelu, false>>(tiles, kThreads * G, shm, p, s);
+    return bf16_out ? launch<gated_bwd_kernel<T, NS, G, kActSilu, true>>(tiles, kThreads * G, shm, p, s)
+                    : launch<gated_bwd_kernel<T, NS, G, kActSilu, false>>(tiles, kThreads * G, shm, p, s);
 }
 
 }  // namespace
 
+// The choice of tiles, times on 256 CUs.  Large tiles win where they fill the
+// CUs; below that the number of CUs reached decides, and where even small
+// tiles leave some idle, groups of waves split a tile's slabs:
+//   rows x F x K        large    128 rows   128, 2 groups   64, 4 groups
+//   256 x 4096 x 4096   50 us    43 us      38 us           29 us   (256 tiles of 64 rows)
+//   512 x 4096 x 2048   31 us    27 us      25 us           33 us   (256 of 128)
+//   1024 x 4096 x 4096  67 us    84 us      83 us          106 us   (512 of 128)
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s) {
     auto al8 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 8 == 0; };
-    if (p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales) && al8(p.u.scales))
-        return launch_gated_gemm_big(p, act, bf16_out, s);
-    if (act == kActGelu) return bf16_out ? fwd<kActGelu, true>(p, s) : fwd<kActGelu, false>(p, s);
-    return bf16_out ? fwd<kActSilu, true>(p, s) : fwd<kActSilu, false>(p, s);
+    const bool large = p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales) && al8(p.u.scales);
+    const int64_t cus = device_cus(s);
+    if (tiles_of(p.M, p.N, 64, kBF) <= cus) return fwd<64, 2, 4>(p, act, bf16_out, s);
+    if (tiles_of(p.M, p.N, 128, kBF) <= cus) return fwd<128, 3, 2>(p, act, bf16_out, s);
+    if (large) return launch_gated_gemm_big(p, act, bf16_out, s);
+    return fwd<128, 3, 1>(p, act, bf16_out, s);
 }
 
+// As above:
+//   rows x F x K        large    128     128, 2 groups   64      64, 2 groups
+//   256 x 4096 x 4096   64 us    41 us   39 us           22 us   22 us    (256 tiles of 64)
+//   512 x 4096 x 2048   43 us    27 us   26 us           20 us   23 us    (512 of 64)
+//   1024 x 4096 x 4096  66 us    46 us   43 us           66 us   70 us    (256 of 128)
+//   2048 x 4096 x 1536  41 us    36 us   43 us           48 us   70 us    (512 of 128)
+//   512 x 14336 x 4096  78 us    86 us   98 us          136 us  153 us    (448 of 128)
+// The last two differ in K: the large tile spends about 25 us beside its
+// slabs, two small ones on a CU about 7 us, but more on each slab.
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
+    const Mx8GemmParams &mm = p.mm;
     auto al4 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
     // (the large tiles' row offsets are 32 bits wide)
     const int64_t lim = (int64_t)1 << 24;
-    if (p.mm.K % 128 == 0 && p.mm.K < lim && p.mm.N < lim && al4(p.mm.a_scales) && al4(p.mm.b_scales))
-        return launch_gated_bwd_big(p, act, bf16_out, s);
-    if (act == kActGelu) return bf16_out ? bwd<kActGelu, true>(p, s) : bwd<kActGelu, false>(p, s);
-    return bf16_out ? bwd<kActSilu, true>(p, s) : bwd<kActSilu, false>(p, s);
+    const bool large = mm.K % 128 == 0 && mm.K < lim && mm.N < lim && al4(mm.a_scales) && al4(mm.b_scales);
+    const int64_t cus = device_cus(s), t64 = tiles_of(mm.M, mm.N, 64, 64), t128 = tiles_of(mm.M, mm.N, 128, 128);
+    if (t64 <= cus) return bwd<64, 3, 2>(p, act, bf16_out, s);
+    if (t64 <= 2 * cus) return bwd<64, 3, 1>(p, act, bf16_out, s);
+    if (t128 <= cus) return bwd<128, 2, 2>(p, act, bf16_out, s);
+    if (large && (t128 > 2 * cus || mm.K > 2048)) return launch_gated_bwd_big(p, act, bf16_out, s);
+    return bwd<128, 2, 1>(p, act, bf16_out, s);
 }
 
 }  // namespace bbs
