@@ -61,7 +61,7 @@ __device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n
 }
 
 // ---------------------------------------------------------------------------
-// Up to eight tokens: v_mfma_f32_4x4x4_16b_bf16, sixteen independent 4 x 4 x 4
+// Up to four tokens: v_mfma_f32_4x4x4_16b_bf16, sixteen independent 4 x 4 x 4
 // products.  Lane 4b + i feeds product b: token i's activations and weight row
 // i's codes at the same four K values, and receives column i (its own row) for
 // the four tokens.  So a lane that holds 16 consecutive codes of one row needs
@@ -74,24 +74,24 @@ __device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n
 // ---------------------------------------------------------------------------
 constexpr int kStepK = 512;
 
-template <int NM, int NG, int R>
+template <int NM, int R>
 struct Step {
     uint4 w[NM][R];          // 32 codes
     uint32_t s[NM][R];       // two E4M3 bytes or one E8M0 byte
-    uint4 x[NG][4];          // 32 activations of one token
+    uint4 x[4];              // 32 activations of one token
 };
 
 // The lane's places in a step, set once: byte offsets of its rows from the
-// workgroup's first row, and its tokens' activations.
-template <int NG, int R>
+// workgroup's first row, and its token's activations.
+template <int R>
 struct Place {
     uint32_t code[R], scale[R];
-    const uint16_t *x[NG];
+    const uint16_t *x;
 };
 
-template <int SC, int NM, int NG, int R>
-__device__ __forceinline__ Place<NG, R> place_of(const GemvParams &p, int64_t n0) {
-    Place<NG, R> pl;
+template <int SC, int R>
+__device__ __forceinline__ Place<R> place_of(const GemvParams &p, int64_t n0) {
+    Place<R> pl;
     const int lane = threadIdx.x & 63, i = lane & 3, b = lane >> 2;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -102,8 +102,7 @@ __device__ __forceinline__ Place<NG, R> place_of(const GemvParams &p, int64_t n0
                       : SC == kRows32 ? row * (uint32_t)(p.K / 32) + b
                                       : b * 2;
     }
-#pragma unroll
-    for (int g = 0; g < NG; ++g) pl.x[g] = p.x + min((int64_t)(4 * g + i), p.T - 1) * p.ldx + b * 32;
+    pl.x = p.x + min((int64_t)i, p.T - 1) * p.ldx + b * 32;
     return pl;
 }
 
@@ -111,9 +110,9 @@ __device__ __forceinline__ Place<NG, R> place_of(const GemvParams &p, int64_t n0
 // first, or none.  It loads the halves from wherever they are or, past the
 // end, from the row's last one, and clears what does not belong to it: no
 // load waits behind a branch.
-template <int SC, int NM, int NG, int R, bool TAIL>
-__device__ __forceinline__ void load_step(Step<NM, NG, R> &st, const GemvParams &p,
-                                          const Place<NG, R> &pl, int64_t n0, int64_t step) {
+template <int SC, int NM, int R, bool TAIL>
+__device__ __forceinline__ void load_step(Step<NM, R> &st, const GemvParams &p, const Place<R> &pl,
+                                          int64_t n0, int64_t step) {
     const int b = (threadIdx.x & 63) >> 2;
     const int64_t k0 = step * kStepK;
     // TAIL: the lane's halves (16-value units from k0) as loaded
@@ -150,18 +149,15 @@ __device__ __forceinline__ void load_step(Step<NM, NG, R> &st, const GemvParams 
             }
         }
     }
+    const uint4 *xr = reinterpret_cast<const uint4 *>(pl.x + k0) - 4 * (TAIL ? b : 0);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const uint4 *xr = reinterpret_cast<const uint4 *>(pl.x[g] + k0) - 4 * (TAIL ? b : 0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (!TAIL) {
-                st.x[g][q] = xr[q];
-            } else {
-                const uint4 v = xr[2 * (q < 2 ? h0 : h1) + (q & 1)];
-                const bool in = q < 2 ? first : second;
-                st.x[g][q] = make_uint4(in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0);
-            }
+    for (int q = 0; q < 4; ++q) {
+        if (!TAIL) {
+            st.x[q] = xr[q];
+        } else {
+            const uint4 v = xr[2 * (q < 2 ? h0 : h1) + (q & 1)];
+            const bool in = q < 2 ? first : second;
+            st.x[q] = make_uint4(in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0);
         }
     }
 }
@@ -180,31 +176,24 @@ __device__ __forceinline__ s16x4 codes4(uint32_t w, int h) {
                                                 __builtin_bit_cast(uint32_t, b)));
 }
 
-// TT tokens are computed (1, 2, 4 or 8), those from p.T on are not stored.
+// TT tokens are computed (1, 2 or 4), those from p.T on are not stored.
 template <int SC, int NM, int TT, int R>
-__device__ __forceinline__ void add_step(float (&acc)[NM][R][TT], const Step<NM, (TT + 3) / 4, R> &st) {
-    constexpr int NG = (TT + 3) / 4, NT = TT < 4 ? TT : 4;
+__device__ __forceinline__ void add_step(float (&acc)[NM][R][TT], const Step<NM, R> &st) {
 #pragma unroll
     for (int hb = 0; hb < 2; ++hb)                       // the lane's two 16-value halves
 #pragma unroll
         for (int w = 0; w < NM; ++w)
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                s16x4 cw[4];
+                f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) cw[q] = codes4(word(st.w[w][r], 2 * hb + (q >> 1)), q & 1);
+                for (int q = 0; q < 4; ++q)
+                    d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(half_of(st.x[2 * hb + (q >> 1)], q & 1),
+                                                               codes4(word(st.w[w][r], 2 * hb + (q >> 1)), q & 1),
+                                                               d, 0, 0, 0);
                 const float sc = SC == kRows32 ? e8m0_value(st.s[w][r]) : e4m3_value(st.s[w][r] >> (8 * hb));
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(half_of(st.x[g][2 * hb + (q >> 1)], q & 1),
-                                                                   cw[q], d, 0, 0, 0);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-                        acc[w][r][4 * g + t] = __builtin_fmaf(d[t], sc, acc[w][r][4 * g + t]);
-                }
+                for (int t = 0; t < TT; ++t) acc[w][r][t] = __builtin_fmaf(d[t], sc, acc[w][r][t]);
             }
 }
 
@@ -222,20 +211,20 @@ constexpr int kFewSplit = 8;     // most waves of a workgroup (K splits)
 
 template <int SC, int NM, int TT, int R>
 __global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) {
-    constexpr int NG = (TT + 3) / 4, NO = TT * R * 4;    // outputs, of NM sums each
+    constexpr int NO = TT * R * 4;                       // outputs, of NM sums each
     __shared__ float part[kFewSplit][NM * NO];
     const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * (4 * R);
     const int64_t full = p.K / kStepK;
-    const Place<NG, R> pl = place_of<SC, NM, NG, R>(p, n0);
+    const Place<R> pl = place_of<SC, R>(p, n0);
     float acc[NM][R][TT] = {};
     int64_t s = wave;
     if (s < full) {
-        Step<NM, NG, R> cur, nxt;
-        load_step<SC, NM, NG, R, false>(cur, p, pl, n0, s);
+        Step<NM, R> cur, nxt;
+        load_step<SC, NM, R, false>(cur, p, pl, n0, s);
         for (; s + nw < full; s += nw) {
-            load_step<SC, NM, NG, R, false>(nxt, p, pl, n0, s + nw);
+            load_step<SC, NM, R, false>(nxt, p, pl, n0, s + nw);
             add_step<SC, NM, TT, R>(acc, cur);
             cur = nxt;
         }
@@ -243,8 +232,8 @@ __global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) 
         s += nw;
     }
     if (s == full && p.K % kStepK) {
-        Step<NM, NG, R> last;
-        load_step<SC, NM, NG, R, true>(last, p, pl, n0, s);
+        Step<NM, R> last;
+        load_step<SC, NM, R, true>(last, p, pl, n0, s);
         add_step<SC, NM, TT, R>(acc, last);
     }
 #pragma unroll
@@ -268,7 +257,7 @@ __global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) 
 }
 
 // ---------------------------------------------------------------------------
-// Nine tokens and more: v_mfma_f32_16x16x32_bf16, sixteen weight rows by
+// Five tokens and more: v_mfma_f32_16x16x32_bf16, sixteen weight rows by
 // sixteen tokens.  Code x scale is exact in BF16 (at most 6 significant bits
 // for E2M1 x E4M3), so the weights are expanded once and serve every token
 // tile.  A wave's step is 128 K values of its row tiles: lane 16 g + i reads
@@ -282,7 +271,7 @@ __global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) 
 // one fragment read fall on sixteen different bank groups.
 // ---------------------------------------------------------------------------
 constexpr int kTileK = 128;
-constexpr int kTileSplit = 8;
+constexpr int kTileSplit = 8;    // most waves of a workgroup (K splits)
 
 // Eight codes of a word times their block scale, in BF16.
 template <int SC>
@@ -412,9 +401,10 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
 #pragma unroll
             for (int t = 0; t < NT; ++t) acc[w][r][t] = f32x4{0, 0, 0, 0};
 
+    const int64_t full = p.K / kTileK;
     TileWeights<NM, NR> tw;
-    int64_t k0 = (int64_t)wave * kTileK;
-    for (; k0 + kTileK <= p.K; k0 += (int64_t)nw * kTileK) {
+    for (int64_t at = wave; at < full; at += nw) {
+        const int64_t k0 = at * kTileK;
         load_weights<SC, NM, NR, false>(tw, p, pl, n0, k0);
         // the wave's reads of the step before are done
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -425,7 +415,8 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
             return *reinterpret_cast<const bf16x8 *>(xl + (16 * t + i) * 256 + 16 * ((4 * g + j) ^ i));
         });
     }
-    if (k0 < p.K) {
+    if (full % nw == wave && p.K % kTileK) {
+        const int64_t k0 = full * kTileK;
         load_weights<SC, NM, NR, true>(tw, p, pl, n0, k0);
         const int left = (int)(p.K - k0) / 8;             // chunks of a token inside K
         tile_products<SC, NM, NT, NR>(acc, tw, [&](int t, int j) {
@@ -495,36 +486,29 @@ hipError_t tile(const GemvParams &p, hipStream_t s) {
 // Rows of a workgroup, over both matrices of the gated form: 16 where that
 // still gives every CU one (one token, 4096 x 14336: 8.1 us with 16 rows, 8.4
 // with 8), 8 below (1536 x 4096: 3.2 us with 8 rows, 3.7 with 16, 3.4 with 4).
-// Eight tokens hold twice the sums and take 8.
 template <int SC, int NM, int TT>
 hipError_t few_rows(const GemvParams &p, hipStream_t s) {
-    const bool many = p.N >= 4096;
-    if constexpr (NM == 1) {
-        if constexpr (TT < 8)
-            if (many) return few<SC, NM, TT, 4>(p, s);
-        return few<SC, NM, TT, 2>(p, s);
-    } else {
-        return many ? few<SC, NM, TT, 2>(p, s) : few<SC, NM, TT, 1>(p, s);
-    }
+    return p.N >= 4096 ? few<SC, NM, TT, 4 / NM>(p, s) : few<SC, NM, TT, 2 / NM>(p, s);
 }
 
 // Row tiles of a workgroup, over both matrices: each re-reads the activations
-// once for all its rows, so as many as leave about a workgroup a CU (48
-// tokens, MXFP4 14336 x 4096: 18.1 us with 64 rows, 23.0 with 32, 29.9 with
-// 16; gated 13 tokens 1536 x 4096: 6.9 us with 16 + 16 rows, 11.0 with 32 + 32).
+// once for all its rows, so four where that leaves about a workgroup a CU (48
+// tokens, MXFP4 14336 x 4096: 18.5 us with 64 rows, 22.5 with 32, 30.8 with
+// 16), and as few as there are below (32 tokens, 4096 x 14336: 16.3 us with 16
+// rows, 18.4 with 32; 64 tokens, 1536 x 4096: 8.2 and 10.5 us).
 template <int SC, int NM, int NT>
 hipError_t tile_rows(const GemvParams &p, hipStream_t s) {
-    if (p.N >= 8192) return tile<SC, NM, NT, 4 / NM>(p, s);
-    if (p.N >= 4096 || NM == 2) return tile<SC, NM, NT, 2 / NM>(p, s);
-    return tile<SC, NM, NT, 1>(p, s);
+    return p.N >= 8192 ? tile<SC, NM, NT, 4 / NM>(p, s) : tile<SC, NM, NT, 1>(p, s);
 }
 
+// Up to four tokens take the 4x4x4 form (three, 14336 x 4096: 11.3 us against
+// 12.4), more the 16x16x32 form (six, 1536 x 4096: 4.5 us against 4.9; eight,
+// 14336 x 4096: 10.1 against 19.5).
 template <int SC, int NM>
 hipError_t run(const GemvParams &p, hipStream_t s) {
     if (p.T == 1) return few_rows<SC, NM, 1>(p, s);
     if (p.T == 2) return few_rows<SC, NM, 2>(p, s);
     if (p.T <= 4) return few_rows<SC, NM, 4>(p, s);
-    if (p.T <= 8) return few_rows<SC, NM, 8>(p, s);
     if (p.T <= 16) return tile_rows<SC, NM, 1>(p, s);
     if (p.T <= 32) return tile_rows<SC, NM, 2>(p, s);
     if (p.T <= 48) return tile_rows<SC, NM, 3>(p, s);
