@@ -37,6 +37,18 @@ __device__ __forceinline__ const uint8_t *word_of(const uint8_t *p) {
 }
 __device__ __forceinline__ const uint8_t *lesser(const uint8_t *a, const uint8_t *b) { return a < b ? a : b; }
 
+// Tile of workgroup b: workgroup b runs on XCD b % 8, so each XCD is given a
+// contiguous range of tile ids, and ids walk 8 row tiles down before moving
+// along the columns, which keeps operand panels in one XCD's L2.
+__device__ __forceinline__ void tile_of(int64_t tm, int64_t tn, int64_t &mt, int64_t &nt) {
+    const int64_t total = tm * tn, x = blockIdx.x % 8, share = total / 8, extra = total % 8;
+    const int64_t id = x * share + (x < extra ? x : extra) + blockIdx.x / 8;
+    const int64_t g = id / (8 * tn), in = id - g * (8 * tn);
+    const int64_t gm = tm - g * 8 < 8 ? tm - g * 8 : 8;
+    mt = g * 8 + in % gm;
+    nt = in / gm;
+}
+
 // Adds the sums of groups 1 .. G - 1 to group 0's, in that order.
 template <int G, int NV>
 __device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, int lane, float (&v)[NV]) {
@@ -73,9 +85,10 @@ struct FwdStage {
 __device__ __forceinline__ int b_column(int r) { return 32 * (r >> 6) + (r & 31); }
 
 template <int TM, int NS, int G, int ACT, bool BF16_OUT>
-__global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p) {
+__global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_kernel(GatedParams p) {
     constexpr int RA = TM / 64;                    // 32-row blocks of a wave
-    constexpr int kIssued = RA + 2 + 3;            // copies one wave issues a slab
+    constexpr int SG = TM > 128 ? 2 : 1;           // groups of 64 scale rows a wave copies
+    constexpr int kIssued = RA + 2 + 3 * SG;       // copies one wave issues a slab
     constexpr int AHEAD = NS - 1;                  // slabs in flight beyond the one consumed
     extern __shared__ __align__(16) uint8_t smem[];
     // four waves a group; group g of G takes slabs g, g + G, ... in its own ring
@@ -83,8 +96,10 @@ __global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p)
     FwdStage<TM> *const st = reinterpret_cast<FwdStage<TM> *>(smem) + grp * NS;
     const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t tm = (p.M + TM - 1) / TM;
-    const int64_t m0 = blockIdx.x % tm * TM, n0 = blockIdx.x / tm * kBF;
+    int64_t m0, n0;
+    tile_of((p.M + TM - 1) / TM, (p.N + kBF - 1) / kBF, m0, n0);
+    m0 *= TM;
+    n0 *= kBF;
     const int64_t kb = p.K / 2, ks = p.K / 16;
     const int64_t nslab = (p.K + 127) / 128;
     const int tail = (int)(p.K % 128);             // K values of a partial last slab, 0: none
@@ -105,8 +120,8 @@ __global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p)
         bsrc[q] = W.codes + min(n0 + b_column(r), p.N - 1) * kb + 16 * pos;
         bend[q] = W.codes + p.N * kb - 16;
     }
-    // scales: wave w copies the words of rows 64 w .. 64 w + 63 (the waves past
-    // the last row repeat the last 64)
+    // scales: the words of a row's bytes, 64 rows a copy (the waves past the
+    // last row repeat the last 64)
     auto scale_row = [&](int r) -> const uint8_t * {
         if (r < TM) {
             const int64_t m = min(m0 + r, p.M - 1);
@@ -116,14 +131,16 @@ __global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p)
         const int64_t n = min(n0 + b_column(r - TM), p.N - 1);
         return W.scales + (W.tile2d ? n / 16 : n) * ks;
     };
-    const int sgroup = min(wave, (TM + 2 * kBF) / 64 - 1) * 64;
-    const uint8_t *ssrc, *slast;
-    {
-        const int r = sgroup + lane;
+    int sgroup[SG];
+    const uint8_t *ssrc[SG], *slast[SG];
+#pragma unroll
+    for (int k = 0; k < SG; ++k) {
+        sgroup[k] = min(wave * SG + k, (TM + 2 * kBF) / 64 - 1) * 64;
+        const int r = sgroup[k] + lane;
         const Fp4View &W = r < TM ? p.a : (((r - TM) >> 5) & 1) ? p.u : p.b;
         const int64_t rows = r < TM ? p.a.rows : p.N;
-        ssrc = word_of(scale_row(r));
-        slast = word_of(W.scales + (W.tile2d ? rows / 16 : rows) * ks - 1);
+        ssrc[k] = word_of(scale_row(r));
+        slast[k] = word_of(W.scales + (W.tile2d ? rows / 16 : rows) * ks - 1);
     }
     auto issue = [&](int64_t s, int stage) {
         FwdStage<TM> &d = st[stage];
@@ -136,7 +153,9 @@ __global__ __launch_bounds__(kThreads * G) void gated_gemm_kernel(GatedParams p)
         for (int q = 0; q < 2; ++q)
             copy_lds16(partial ? lesser(bsrc[q] + at, bend[q]) : bsrc[q] + at, d.b + (wave * 2 + q) * 1024);
 #pragma unroll
-        for (int w = 0; w < 3; ++w) copy_lds4(lesser(ssrc + s * 8 + 4 * w, slast), &d.sc[w][sgroup]);
+        for (int k = 0; k < SG; ++k)
+#pragma unroll
+            for (int w = 0; w < 3; ++w) copy_lds4(lesser(ssrc[k] + s * 8 + 4 * w, slast[k]), &d.sc[w][sgroup[k]]);
     };
 
     // the lane's fragment rows and the byte shift of their scales
@@ -299,8 +318,10 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
     const Mx8GemmParams &mm = p.mm;
     const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
-    const int64_t tm = (mm.M + T - 1) / T;
-    const int64_t m0 = blockIdx.x % tm * T, n0 = blockIdx.x / tm * T;
+    int64_t m0, n0;
+    tile_of((mm.M + T - 1) / T, (mm.N + T - 1) / T, m0, n0);
+    m0 *= T;
+    n0 *= T;
     const int64_t nkb = mm.K / 32, nslab = (mm.K + 127) / 128;
     const int tail = (int)(mm.K % 128);
 
@@ -463,11 +484,14 @@ hipError_t bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
 
 // The choice of tiles, times on 256 CUs.  Large tiles win where they fill the
 // CUs; below that the number of CUs reached decides, and where even small
-// tiles leave some idle, groups of waves split a tile's slabs:
-//   rows x F x K        large    128 rows   128, 2 groups   64, 4 groups
-//   256 x 4096 x 4096   50 us    43 us      38 us           29 us   (256 tiles of 64 rows)
-//   512 x 4096 x 2048   31 us    27 us      25 us           33 us   (256 of 128)
-//   1024 x 4096 x 4096  67 us    84 us      83 us          106 us   (512 of 128)
+// tiles leave some idle, groups of waves split a tile's slabs.  Two 256-row
+// workgroups share a CU (their registers are held to half) and stand in for
+// the large tiles where K or the scales' alignment rules those out.
+//   rows x F x K        large    256 rows   128 rows, 2 groups   64, 4 groups
+//   256 x 4096 x 4096   50 us               38 us                29 us   (256 tiles of 64 rows)
+//   512 x 4096 x 2048   31 us               25 us                33 us   (256 of 128)
+//   1024 x 4096 x 4096  68 us    71 us      81 us                        (512 of 128)
+//   4096 x 4096 x 4096  203 us   246 us     304 us
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s) {
     auto al8 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 8 == 0; };
     const bool large = p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales) && al8(p.u.scales);
@@ -475,7 +499,7 @@ hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipSt
     if (tiles_of(p.M, p.N, 64, kBF) <= cus) return fwd<64, 2, 4>(p, act, bf16_out, s);
     if (tiles_of(p.M, p.N, 128, kBF) <= cus) return fwd<128, 3, 2>(p, act, bf16_out, s);
     if (large) return launch_gated_gemm_big(p, act, bf16_out, s);
-    return fwd<128, 3, 1>(p, act, bf16_out, s);
+    return fwd<256, 2, 1>(p, act, bf16_out, s);
 }
 
 // As above:
@@ -486,18 +510,19 @@ hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipSt
 //   2048 x 4096 x 1536  41 us    36 us   43 us           48 us   70 us    (512 of 128)
 //   512 x 14336 x 4096  78 us    86 us   98 us          136 us  153 us    (448 of 128)
 // The last two differ in K: the large tile spends about 25 us beside its
-// slabs, two small ones on a CU about 7 us, but more on each slab.
+// slabs, two small ones on a CU about 7 us, but more on each slab.  Where K is
+// no multiple of 128 the large tile's rows lie across cache lines, and it
+// wins later (4096 x 4096 x 4000: 140 us against 176; 1536 x 6016 x 2016, 564
+// tiles of 128: 78 against 66).
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
     const Mx8GemmParams &mm = p.mm;
-    auto al4 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
-    // (the large tiles' row offsets are 32 bits wide)
-    const int64_t lim = (int64_t)1 << 24;
-    const bool large = mm.K % 128 == 0 && mm.K < lim && mm.N < lim && al4(mm.a_scales) && al4(mm.b_scales);
+    const int64_t lim = (int64_t)1 << 24;          // the large tiles' row offsets are 32 bits wide
     const int64_t cus = device_cus(s), t64 = tiles_of(mm.M, mm.N, 64, 64), t128 = tiles_of(mm.M, mm.N, 128, 128);
     if (t64 <= cus) return bwd<64, 3, 2>(p, act, bf16_out, s);
     if (t64 <= 2 * cus) return bwd<64, 3, 1>(p, act, bf16_out, s);
     if (t128 <= cus) return bwd<128, 2, 2>(p, act, bf16_out, s);
-    if (large && (t128 > 2 * cus || mm.K > 2048)) return launch_gated_bwd_big(p, act, bf16_out, s);
+    const bool large = mm.K % 128 == 0 ? t128 > 2 * cus || mm.K > 2048 : t128 > 3 * cus;
+    if (large && mm.K < lim && mm.N < lim) return launch_gated_bwd_big(p, act, bf16_out, s);
     return bwd<128, 2, 1>(p, act, bf16_out, s);
 }
 

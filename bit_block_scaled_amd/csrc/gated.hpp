@@ -50,7 +50,7 @@ struct GemvParams {
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
 // The large-tile kernel (K % 128 == 0, 16-byte aligned codes, 8-byte aligned scales).
 hipError_t launch_gated_gemm_big(const GatedParams &p, int act, bool bf16_out, hipStream_t s);
-// The same for the backward pass (K % 128 == 0, 4-byte aligned scales).
+// The same for the backward pass (any K, K and N below 2^24).
 hipError_t launch_gated_bwd_big(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s);
 hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s);

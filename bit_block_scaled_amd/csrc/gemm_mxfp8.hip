@@ -49,16 +49,19 @@ constexpr int BM = 256, BN = 256, BK = 128, NT = 256;
 constexpr int GROUP_M = 8;
 
 // BK is in bytes of a row: 128 FP8 values or 256 FP4 values per slab.
-template <bool FP4>
+// ANYK: FP8 with K any multiple of 32.  The last slab may then be partial, and
+// a row's scale bytes may start at any byte: the two aligned words that hold
+// a slab's four bytes are copied, and shifted into place when they are read.
+template <bool FP4, bool ANYK = false>
 struct Stage {
     uint8_t a[BM * BK];
     uint8_t b[BN * BK];
-    uint32_t as[FP4 ? 2 : 1][BM];   // the slab's E8M0 bytes per row: 4 (FP8) or 8 (FP4)
-    uint32_t bs[FP4 ? 2 : 1][BN];
+    uint32_t as[FP4 || ANYK ? 2 : 1][BM];   // the slab's E8M0 bytes per row: 4 (FP8) or 8 (FP4)
+    uint32_t bs[FP4 || ANYK ? 2 : 1][BN];
 };
-template <bool FP4>
+template <bool FP4, bool ANYK = false>
 struct Smem {
-    Stage<FP4> st[2];
+    Stage<FP4, ANYK> st[2];
 };
 
 // Scale bytes (= 32-blocks) per row in one slab.
@@ -77,7 +80,12 @@ struct Plan {
     uint32_t sa_off, sb_off;
 };
 
-template <bool FP4>
+// The aligned word at or before x.
+__device__ __forceinline__ const uint8_t *word_of(const uint8_t *x) {
+    return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(x) & ~(uintptr_t)3);
+}
+
+template <bool FP4, bool ANYK = false>
 __device__ __forceinline__ Plan make_plan(const Mx8GemmParams &p, int64_t m0, int64_t n0) {
     Plan pl;
     const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -104,33 +112,57 @@ __device__ __forceinline__ Plan make_plan(const Mx8GemmParams &p, int64_t m0, in
     const int srow = FP4 ? t : (t >> 7) * 128 + ((t & 7) ^ ((s_rl >> 3) << 2)) * 16 + s_rl;
     pl.sa_off = (uint32_t)((min(m0 + srow, p.M - 1) - m0) * nkb);
     pl.sb_off = (uint32_t)((min(n0 + srow, p.N - 1) - n0) * nkb);
+    if (ANYK) {
+        const uint8_t *a0 = word_of(pl.sa_base), *b0 = word_of(pl.sb_base);
+        pl.sa_off = (uint32_t)(word_of(pl.sa_base + pl.sa_off) - a0);
+        pl.sb_off = (uint32_t)(word_of(pl.sb_base + pl.sb_off) - b0);
+        pl.sa_base = a0;
+        pl.sb_base = b0;
+    }
     return pl;
 }
 
+// ANYK: the last addresses a code copy (16 bytes) and a scale copy (a word) of
+// the operands may have.
+struct Ends {
+    const uint8_t *a, *b, *sa, *sb;
+};
+
+__device__ __forceinline__ Ends ends_of(const Mx8GemmParams &p) {
+    const int64_t nkb = p.K / 32;
+    return {p.a_codes + p.M * p.K - 16, p.b_codes + p.N * p.K - 16,
+            word_of(p.a_scales + p.M * nkb - 1), word_of(p.b_scales + p.N * nkb - 1)};
+}
+
+__device__ __forceinline__ const uint8_t *lesser(const uint8_t *x, const uint8_t *y) { return x < y ? x : y; }
+
 // The scale copies of slab s (4 bytes per row per copy).
-template <bool FP4>
-__device__ __forceinline__ void issue_scales(Stage<FP4> &st, const Plan &pl, int64_t s) {
+template <bool FP4, bool ANYK>
+__device__ __forceinline__ void issue_scales(Stage<FP4, ANYK> &st, const Plan &pl, int64_t s,
+                                             const Ends &ends = {}) {
     const int w = threadIdx.x >> 6;
     const int64_t blk = s * slab_blocks<FP4>();
 #pragma unroll
-    for (int h = 0; h < (FP4 ? 2 : 1); ++h) {
-        copy_lds4(pl.sa_base + blk + 4 * h + pl.sa_off, st.as[h] + w * 64);
-        copy_lds4(pl.sb_base + blk + 4 * h + pl.sb_off, st.bs[h] + w * 64);
+    for (int h = 0; h < (FP4 || ANYK ? 2 : 1); ++h) {
+        const uint8_t *a = pl.sa_base + blk + 4 * h + pl.sa_off, *b = pl.sb_base + blk + 4 * h + pl.sb_off;
+        copy_lds4(ANYK ? lesser(a, ends.sa) : a, st.as[h] + w * 64);
+        copy_lds4(ANYK ? lesser(b, ends.sb) : b, st.bs[h] + w * 64);
     }
 }
 
 // Enqueue the copies of slab s into one LDS stage (asynchronous).
-template <bool FP4>
-__device__ __forceinline__ void issue(Stage<FP4> &st, const Plan &pl, int64_t s) {
+template <bool FP4, bool ANYK>
+__device__ __forceinline__ void issue(Stage<FP4, ANYK> &st, const Plan &pl, int64_t s, const Ends &ends = {}) {
     const int w = threadIdx.x >> 6;
     const int64_t k0 = s * BK;                          // byte offset in a row
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         const int seg = (w * 8 + q) * 1024;
-        copy_lds16(pl.a_base + k0 + pl.a_off[q], st.a + seg);
-        copy_lds16(pl.b_base + k0 + pl.b_off[q], st.b + seg);
+        const uint8_t *a = pl.a_base + k0 + pl.a_off[q], *b = pl.b_base + k0 + pl.b_off[q];
+        copy_lds16(ANYK ? lesser(a, ends.a) : a, st.a + seg);
+        copy_lds16(ANYK ? lesser(b, ends.b) : b, st.b + seg);
     }
-    issue_scales(st, pl, s);
+    issue_scales(st, pl, s, ends);
 }
 
 // One 16-byte chunk c of row r (FP4: the 32 values of one block); the upper
@@ -166,10 +198,16 @@ constexpr int kIssued8 = 18;
 // wave's reads are all issued; after one barrier at shell 6 the stage is free
 // and the copies of slab sn (two slabs ahead) go into it during shells 6-7:
 // they get most of two slabs to land, where copying into the other stage of a
-// two-stage ring gives them one.  kn: byte offset of the copied codes.
-__device__ __forceinline__ void compute_held(Stage<false> &st, f32x4 (&acc)[8][8], int wm,
+// two-stage ring gives them one.  kn: byte offset of the copied codes.  ANYK:
+// shift holds the byte shifts of the lane's A and B scale words (the rows rl +
+// 16 k of a side share theirs), keep clears the scales of blocks past K, and
+// LAST says that slab sn is the last one, whose copies must stay inside the
+// operands.
+template <bool ANYK = false, bool LAST = false>
+__device__ __forceinline__ void compute_held(Stage<false, ANYK> &st, f32x4 (&acc)[8][8], int wm,
                                              int wn, int lane, const Plan &pl, int64_t sn,
-                                             int64_t kn) {
+                                             int64_t kn, const Ends &ends = {}, uint2 shift = {},
+                                             uint32_t keep = ~0u) {
     const int w = threadIdx.x >> 6;
     const int g = lane >> 4, rl = lane & 15;
     i32x8 af[8], bf[8];
@@ -187,8 +225,21 @@ __device__ __forceinline__ void compute_held(Stage<false> &st, f32x4 (&acc)[8][8
     read(0);
     read(1);
     __builtin_amdgcn_sched_barrier(0);
-    const uint32_t saw[8] = {sa0.x, sa0.y, sa0.z, sa0.w, sa1.x, sa1.y, sa1.z, sa1.w};
-    const uint32_t sbw[8] = {sb0.x, sb0.y, sb0.z, sb0.w, sb1.x, sb1.y, sb1.z, sb1.w};
+    uint32_t saw[8] = {sa0.x, sa0.y, sa0.z, sa0.w, sa1.x, sa1.y, sa1.z, sa1.w};
+    uint32_t sbw[8] = {sb0.x, sb0.y, sb0.z, sb0.w, sb1.x, sb1.y, sb1.z, sb1.w};
+    if constexpr (ANYK) {
+        auto join = [&](uint32_t *w, const uint32_t *next, uint32_t sh) __attribute__((always_inline)) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(next);
+            const uint32_t n[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __builtin_amdgcn_alignbyte(n[k], w[k], sh) & keep;
+        };
+        join(saw, &st.as[1][wm * 128 + h0], shift.x);
+        join(saw + 4, &st.as[1][wm * 128 + h1], shift.x);
+        join(sbw, &st.bs[1][wn * 128 + h0], shift.y);
+        join(sbw + 4, &st.bs[1][wn * 128 + h1], shift.y);
+        __builtin_amdgcn_sched_barrier(0);
+    }
     auto byte_of = [&](uint32_t v) { return (int)((v >> (8 * g)) & 0xFFu); };
     int c = 0;                                         // copies issued
 #pragma unroll
@@ -213,10 +264,11 @@ __device__ __forceinline__ void compute_held(Stage<false> &st, f32x4 (&acc)[8][8
             if (k == 6 || (k == 7 && (e & 1))) {
                 if (c < 16) {
                     const int q = c >> 1;
-                    if (c & 1) copy_lds16(pl.b_base + kn + pl.b_off[q], st.b + (w * 8 + q) * 1024);
-                    else copy_lds16(pl.a_base + kn + pl.a_off[q], st.a + (w * 8 + q) * 1024);
+                    const uint8_t *src = (c & 1 ? pl.b_base + pl.b_off[q] : pl.a_base + pl.a_off[q]) + kn;
+                    if (LAST) src = lesser(src, c & 1 ? ends.b : ends.a);
+                    copy_lds16(src, (c & 1 ? st.b : st.a) + (w * 8 + q) * 1024);
                 } else if (c == 16) {
-                    issue_scales(st, pl, sn);
+                    issue_scales(st, pl, sn, ends);
                 }
                 ++c;
             }
@@ -347,10 +399,11 @@ struct StoreC {};
 // described where C is stored below.  The ring's last two look-ahead copies,
 // which a plain product spends on repeating its last slab, bring the tile's
 // bytes into LDS: tile 0 while the last slab is multiplied, tile 1 at its end.
-template <bool FP4, bool BF16_OUT, typename Finish = StoreC>
+template <bool FP4, bool BF16_OUT, typename Finish = StoreC, bool ANYK = false>
 __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *smem_raw,
                                             const Finish &finish = Finish{}) {
-    mx::Smem<FP4> &sm = *reinterpret_cast<mx::Smem<FP4> *>(smem_raw);
+    static_assert(!ANYK || !std::is_same_v<Finish, StoreC>, "the plain products take whole slabs");
+    mx::Smem<FP4, ANYK> &sm = *reinterpret_cast<mx::Smem<FP4, ANYK> *>(smem_raw);
     const int64_t tm = (p.M + mx::BM - 1) / mx::BM, tn = (p.N + mx::BN - 1) / mx::BN;
     const int64_t T = tm * tn;
     const int64_t bid = blockIdx.x, x = bid % 8, j = bid / 8;
@@ -363,7 +416,7 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
 
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int wm = wave >> 1, wn = wave & 1;
-    const mx::Plan pl = mx::make_plan<FP4>(p, m0, n0);
+    const mx::Plan pl = mx::make_plan<FP4, ANYK>(p, m0, n0);
 
     // FP8: 8 x 8 blocks of 16 x 16; FP4: 4 x 4 blocks of 32 x 32 (256 FP32 each)
     typedef std::conditional_t<FP4, f32x16[4][4], f32x4[8][8]> Acc;
@@ -382,27 +435,63 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
 
     const int64_t nslab = p.K / (FP4 ? 2 * mx::BK : mx::BK);
     if constexpr (!FP4 && !std::is_same_v<Finish, StoreC>) {
-        auto tile = [&](const uint8_t *x) { return mx::byte_tile_plan(pl, x, p.M, p.N, m0, n0); };
-        mx::issue(sm.st[0], pl, 0);
-        if (nslab > 1) {
-            mx::issue(sm.st[1], pl, 1);
-        } else {
-            mx::issue(sm.st[1], tile(finish.tile0()), 0);
+        constexpr int kIssued = ANYK ? mx::kIssued8 + 2 : mx::kIssued8;
+        const int tail = ANYK ? (int)(p.K % mx::BK) : 0;   // K values of a partial last slab
+        const int64_t nslab = (p.K + mx::BK - 1) / mx::BK;
+        const mx::Ends ends = ANYK ? mx::ends_of(p) : mx::Ends{};
+        uint2 shift = make_uint2(0, 0);
+        if (ANYK) {
+            const int64_t nkb = p.K / 32;
+            shift.x = (uint32_t)(reinterpret_cast<uintptr_t>(p.a_scales) + (m0 + wm * 128 + (lane & 15)) * nkb) & 3u;
+            shift.y = (uint32_t)(reinterpret_cast<uintptr_t>(p.b_scales) + (n0 + wn * 128 + (lane & 15)) * nkb) & 3u;
         }
-        mx::wait_vmcnt<mx::kIssued8>();
+        // a partial last slab, landed: zeros in the chunks past K (they hold
+        // other rows' codes), whose scales are cleared too
+        auto clear_past = [&](mx::Stage<false, ANYK> &st) {
+            const int first = tail / 16, n = 8 - first;
+            for (int e = t; e < 2 * mx::BM * n; e += mx::NT) {
+                const int r = e / n % mx::BM, c = first + e % n;
+                *reinterpret_cast<uint4 *>((e < mx::BM * n ? st.a : st.b) + r * mx::BK + 16 * mx::swz(r, c)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            __syncthreads();
+        };
+        auto tile = [&](const uint8_t *x) { return mx::byte_tile_plan(pl, x, p.M, p.N, m0, n0); };
+        mx::issue(sm.st[0], pl, 0, ends);
+        if (nslab > 1) {
+            mx::issue(sm.st[1], pl, 1, ends);
+        } else {
+            const mx::Plan tp = tile(finish.tile0());
+            mx::Ends open = ends;                     // the tile's own clamps hold for its code copies
+            open.a = open.b = reinterpret_cast<const uint8_t *>(~(uintptr_t)0);
+            mx::issue(sm.st[1], tp, 0, open);
+        }
+        mx::wait_vmcnt<kIssued>();
         __syncthreads();
         __builtin_amdgcn_s_waitcnt(0xC07F);           // no scalar load in flight into the loop
-        for (int64_t s = 0; s + 2 < nslab; ++s) {
-            mx::compute_held(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK);
-            mx::wait_vmcnt<mx::kIssued8>();
+        // slabs 0 .. nslab - 3 copy the slab two ahead; with ANYK the last of
+        // these copies is the one that may end inside a slab
+        const int64_t plain_end = ANYK ? nslab - 3 : nslab - 2;
+        int64_t s = 0;
+        for (; s < plain_end; ++s) {
+            mx::compute_held<ANYK>(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK, ends, shift);
+            mx::wait_vmcnt<kIssued>();
+            __syncthreads();
+        }
+        if (ANYK && nslab > 2) {
+            mx::compute_held<ANYK, true>(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK, ends, shift);
+            mx::wait_vmcnt<kIssued>();
             __syncthreads();
         }
         if (nslab > 1) {
-            mx::compute_held(sm.st[nslab & 1], acc, wm, wn, lane, tile(finish.tile0()), 0, 0);
-            mx::wait_vmcnt<mx::kIssued8>();
+            mx::compute_held<ANYK>(sm.st[nslab & 1], acc, wm, wn, lane, tile(finish.tile0()), 0, 0, ends, shift);
+            mx::wait_vmcnt<kIssued>();
             __syncthreads();
         }
-        mx::compute_held(sm.st[(nslab - 1) & 1], acc, wm, wn, lane, tile(finish.tile1()), 0, 0);
+        if (tail) clear_past(sm.st[(nslab - 1) & 1]);
+        const uint32_t keep = tail ? (1u << (8 * (tail / 32))) - 1 : ~0u;
+        mx::compute_held<ANYK>(sm.st[(nslab - 1) & 1], acc, wm, wn, lane, tile(finish.tile1()), 0, 0, ends, shift,
+                               keep);
         finish(sm.st[nslab & 1].a, sm.st[(nslab - 1) & 1].a, acc, m0, n0, wm, wn, lane);
     } else if constexpr (!FP4) {
         // Slab s lives in stage s % 2 and is copied while slab s - 2 is
@@ -568,10 +657,10 @@ struct GatedBwd {
     }
 };
 
-template <int ACT, bool BF16_OUT>
+template <int ACT, bool BF16_OUT, bool ANYK>
 __global__ __launch_bounds__(mx::NT) void mxfp8_gated_bwd_big_kernel(GatedBwdParams p) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    mx_gemm_big<false, BF16_OUT>(p.mm, smem_raw, GatedBwd<ACT, BF16_OUT>{p});
+    mx_gemm_big<false, BF16_OUT, GatedBwd<ACT, BF16_OUT>, ANYK>(p.mm, smem_raw, GatedBwd<ACT, BF16_OUT>{p});
 }
 
 // The kernel's dynamic LDS limit is raised once per kernel (thread-safe
@@ -591,16 +680,19 @@ static int64_t big_tiles(const Mx8GemmParams &p) {
     return ((p.M + mx::BM - 1) / mx::BM) * ((p.N + mx::BN - 1) / mx::BN);
 }
 
-hipError_t launch_gated_bwd_big(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
-    const size_t shm = sizeof(mx::Smem<false>);
+template <int ACT, bool BF16_OUT>
+static void gated_bwd_big(const GatedBwdParams &p, hipStream_t s) {
     const int64_t T = big_tiles(p.mm);
-    if (act == kActGelu) {
-        if (bf16_out) launch_big<mxfp8_gated_bwd_big_kernel<kActGelu, true>>(shm, p, T, s);
-        else launch_big<mxfp8_gated_bwd_big_kernel<kActGelu, false>>(shm, p, T, s);
-    } else {
-        if (bf16_out) launch_big<mxfp8_gated_bwd_big_kernel<kActSilu, true>>(shm, p, T, s);
-        else launch_big<mxfp8_gated_bwd_big_kernel<kActSilu, false>>(shm, p, T, s);
-    }
+    auto al4 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 4 == 0; };
+    if (p.mm.K % mx::BK == 0 && al4(p.mm.a_scales) && al4(p.mm.b_scales))
+        launch_big<mxfp8_gated_bwd_big_kernel<ACT, BF16_OUT, false>>(sizeof(mx::Smem<false>), p, T, s);
+    else
+        launch_big<mxfp8_gated_bwd_big_kernel<ACT, BF16_OUT, true>>(sizeof(mx::Smem<false, true>), p, T, s);
+}
+
+hipError_t launch_gated_bwd_big(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
+    if (act == kActGelu) bf16_out ? gated_bwd_big<kActGelu, true>(p, s) : gated_bwd_big<kActGelu, false>(p, s);
+    else bf16_out ? gated_bwd_big<kActSilu, true>(p, s) : gated_bwd_big<kActSilu, false>(p, s);
     return hipGetLastError();
 }
 

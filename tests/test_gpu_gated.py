@@ -434,6 +434,182 @@ def test_fp8_group_grid(bbs):
             assert np.array_equal(got, kept), (place, sign, got, kept)
 
 
+# ---------------------------------------------------------------------------
+# Problems of enough tiles for the large-tile kernels, against 64 bits on the
+# GPU.  Operands are decoded from their bytes by torch.
+# ---------------------------------------------------------------------------
+
+E2M1 = [0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6]
+
+
+def nv64(t):
+    n = torch.stack((t.codes & 15, t.codes >> 4), 2).flatten(1).long()
+    v = torch.tensor(E2M1, dtype=torch.float64, device=dev())[n]
+    s = t.scales.view(torch.float8_e4m3fn).double()
+    s = s.repeat_interleave(t.rows // s.shape[0], 0).repeat_interleave(16, 1)
+    return v * s * t.s_dec.double().reshape(-1, 1)
+
+
+def mx64(t):
+    return t.codes.view(torch.float8_e4m3fn).double() * torch.exp2(t.scales.double() - 127).repeat_interleave(32, 1)
+
+
+def act_t(act, g):
+    """act(g), its slope, and their error bounds as gated_ref's, on the GPU."""
+    c = 2 * (2 / np.pi) ** 0.5 if act == "gelu" else 0.0
+    z = c * (g + 0.044715 * g ** 3) if act == "gelu" else g
+    dz = c * (1 + 3 * 0.044715 * g * g) if act == "gelu" else torch.ones_like(g)
+    s, q = torch.sigmoid(z), torch.sigmoid(-z)
+    ag = g.abs()
+    ea = 16 * ULP * ag * s + 6 * ULP * ag * s * q * z.abs() + ag * 2.0 ** -120
+    es = 24 * ULP * (s + ag * s * q * dz) + 6 * ULP * z.abs() * s * q * (1 + ag * dz) + (1 + ag * dz) * 2.0 ** -120
+    return g * s, s + g * s * q * dz, ea, es
+
+
+def product_t(a, b):
+    return a @ b.t(), (a.shape[1] + 32) * ULP * (a.abs() @ b.abs().t())
+
+
+def within(y, ref, E, bf16, what):
+    """FP32 outputs within E; BF16 ones within E and half a BF16 step (2^-8) more."""
+    tol = E + (ref.abs() + E) * 2.0 ** -8 if bf16 else E
+    bad = (y.double() - ref).abs() > tol
+    assert not bool(torch.isnan(y).any()) and not bool(bad.any()), (what, int(bad.sum()), bad.nonzero()[0].tolist())
+
+
+def checkpoint_within(c, ref, E, what):
+    k = torch.exp2(c.scales.double() - 127).repeat_interleave(32, 1)
+    v = mx64(c)
+    a = ref.abs().reshape(len(ref), -1, 32).amax(2)
+    e = E.reshape(len(ref), -1, 32).amax(2)
+    s = torch.exp2(c.scales.double() - 127)
+    assert bool((448 * s >= a - e).all()) and not bool(((224 * s >= a + e) & (c.scales > 0)).any()), what
+    half = torch.maximum((ref.abs() + E) * 2.0 ** -4, k * 2.0 ** -10)
+    assert bool(((v - ref).abs() <= half + E).all()), what
+
+
+def random_nv(bbs, rows, cols, tile2d, seed, shift=0):
+    """Random codes and scales; `shift` moves the scales off their alignment."""
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    codes = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device=dev(), generator=g)
+    n = (rows // 16 if tile2d else rows) * (cols // 16)
+    buf = torch.randint(0x20, 0x48, (n + shift,), dtype=torch.uint8, device=dev(), generator=g)
+    return bbs.NVFP4Tensor(codes, buf[shift:].view(-1, cols // 16), torch.full((1,), 2.0 / cols ** 0.5, device=dev()),
+                           rows, cols, tile2d)
+
+
+def random_mx(bbs, rows, cols, seed, mid=121, shift=0):
+    g = torch.Generator(device=dev()).manual_seed(seed)
+    codes = torch.randint(0, 256, (rows, cols), dtype=torch.uint8, device=dev(), generator=g)
+    codes[(codes & 0x7F) == 0x7F] -= 8                                    # no NaN
+    buf = torch.randint(mid - 4, mid, (rows * (cols // 32) + shift,), dtype=torch.uint8, device=dev(), generator=g)
+    return bbs.MXFP8Tensor(codes, buf[shift:].view(-1, cols // 32), rows, cols)
+
+
+# whole and partial slabs, one to many of them; 1040 x 2080 fills 297 tiles of
+# 128 x 64, so K % 128 == 0 takes the large tiles and the rest the 256-row ones
+LARGE_FWD = [
+    (1040, 2080, 128, True, "silu", True, True, 0),
+    (1040, 2080, 256, False, "gelu", False, True, 0),
+    (1040, 2080, 384, True, "gelu", True, False, 0),
+    (1040, 2080, 1024, True, "silu", False, True, 0),
+    (1040, 2080, 1024, False, "silu", True, True, 3),
+    (1040, 2080, 16, False, "silu", False, True, 0),
+    (1040, 2080, 144, True, "silu", False, True, 1),
+    (1040, 2080, 272, False, "gelu", True, True, 0),
+    (1040, 2080, 400, True, "silu", False, False, 2),
+    (3088, 1552, 1552, False, "silu", True, False, 0),
+    (288, 9024, 640, True, "gelu", True, True, 0),
+]
+
+
+@pytest.mark.parametrize("M,F,K,tile2d,act,bf16,ckpt,shift", LARGE_FWD)
+def test_gated_gemm_large(bbs, M, F, K, tile2d, act, bf16, ckpt, shift):
+    announce(f"gated gemm {M} x {F} x {K} tile2d={tile2d} {act} bf16={bf16} ckpt={ckpt} shift={shift}")
+    A = random_nv(bbs, M, K, False, 1, shift)
+    Wg, Wu = random_nv(bbs, F, K, tile2d, 2, shift), random_nv(bbs, F, K, tile2d, 3, shift)
+    h = torch.full((M, F), 7.0, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+    c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) if ckpt else None for _ in range(2)]
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, int(bf16), act=int(act == "gelu"), g_ckpt=c[0], u_ckpt=c[1])
+    a = nv64(A)
+    (g, Eg), (u, Eu) = product_t(a, nv64(Wg)), product_t(a, nv64(Wu))
+    v, _, ea, _ = act_t(act, g)
+    E = (u.abs() + Eu) * (1.13 * Eg + ea) + v.abs() * Eu + 2 * ULP * (v * u).abs()
+    within(h, v * u, E, bf16, "h")
+    if ckpt:
+        checkpoint_within(c[0], g, Eg, "g8")
+        checkpoint_within(c[1], u, Eu, "u8")
+
+
+# 540 tiles of 128 x 128 take the large tiles for K % 128 == 0, 792 for any K
+LARGE_BWD = [
+    (2500, 3360, 128, "silu", True, 0),
+    (2500, 3360, 256, "gelu", False, 0),
+    (2500, 3360, 384, "silu", False, 1),
+    (2500, 3360, 1024, "gelu", True, 0),
+    (3000, 4128, 32, "silu", False, 0),
+    (3000, 4128, 96, "silu", True, 3),
+    (3000, 4128, 160, "gelu", False, 0),
+    (3000, 4128, 288, "silu", True, 2),
+    (3000, 4128, 480, "silu", False, 0),
+    (3000, 4128, 1056, "gelu", True, 1),
+    (1030, 4128, 2176, "silu", True, 0),
+    (1030, 4128, 608, "silu", False, 1),
+]
+
+
+@pytest.mark.parametrize("M,F,K,act,bf16,shift", LARGE_BWD)
+def test_gated_bwd_large(bbs, M, F, K, act, bf16, shift):
+    announce(f"gated bwd {M} x {F} x {K} {act} bf16={bf16} shift={shift}")
+    dY, Wt = random_mx(bbs, M, K, 4, shift=shift), random_mx(bbs, F, K, 5, shift=shift)
+    g8, u8 = random_mx(bbs, M, F, 6, 122), random_mx(bbs, M, F, 7, 121)
+    d = torch.full((M, 2 * F), 7.0, dtype=torch.bfloat16 if bf16 else torch.float32, device=dev())
+    bbs.mxfp8_gemm_gated_bwd(dY, Wt, g8, u8, d[:, :F], d[:, F:], int(bf16), act=int(act == "gelu"))
+    y, w, g, u = mx64(dY), mx64(Wt), mx64(g8), mx64(u8)
+    dh, Ed = product_t(y, w)
+    # the matrix instruction's grid (product_mx8)
+    ga, gb = (v.abs().reshape(len(v), K // 8, 8).amax(2) for v in (y, w))
+    Ed = Ed + 7 * 2.0 ** -13 * (ga @ gb.t())
+    a, sl, ea, es = act_t(act, g)
+    within(d[:, :F], dh * u * sl, u.abs() * ((dh.abs() + Ed) * es + sl.abs() * Ed) + 3 * ULP * (dh * u * sl).abs(),
+           bf16, "dG")
+    within(d[:, F:], dh * a, (dh.abs() + Ed) * ea + a.abs() * Ed + 2 * ULP * (dh * a).abs(), bf16, "dU")
+
+
+def test_nan_rows_do_not_leak(bbs):
+    """A NaN code in one row of dY or Wt reaches that row's or column's outputs alone,
+    also where K ends inside a slab and a copy runs into the next row."""
+    announce("gated bwd: NaN codes")
+    for M, F, K in ((70, 96, 160), (3000, 4128, 160), (300, 544, 288)):
+        dY, Wt = random_mx(bbs, M, K, 4), random_mx(bbs, F, K, 5)
+        g8, u8 = random_mx(bbs, M, F, 6), random_mx(bbs, M, F, 7)
+        dY.codes[33, :] = 0x7F
+        Wt.codes[64, :] = 0x7F
+        d = torch.empty((M, 2 * F), dtype=torch.float32, device=dev())
+        bbs.mxfp8_gemm_gated_bwd(dY, Wt, g8, u8, d[:, :F], d[:, F:], 0)
+        bad = torch.isnan(d.view(M, 2, F)[:, 1])
+        want = torch.zeros_like(bad)
+        want[33, :] = True
+        want[:, 64] = True
+        assert torch.equal(bad, want), (M, F, K)
+
+
+def test_gated_gemm_output_beyond_32_bits(bbs):
+    """An output of more than 2^32 bytes and 2^31 elements: the last rows."""
+    announce("gated gemm past 2^31 outputs")
+    M, F, K = 65552, 32800, 128
+    A, Wg, Wu = random_nv(bbs, M, K, False, 1), random_nv(bbs, F, K, True, 2), random_nv(bbs, F, K, True, 3)
+    h = torch.empty((M, F), dtype=torch.bfloat16, device=dev())
+    c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) for _ in range(2)]
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, 1, g_ckpt=c[0], u_ckpt=c[1])
+    a = nv64(A)[-48:]
+    (g, Eg), (u, Eu) = product_t(a, nv64(Wg)), product_t(a, nv64(Wu))
+    v, _, ea, _ = act_t("silu", g)
+    within(h[-48:], v * u, (u.abs() + Eu) * (1.13 * Eg + ea) + v.abs() * Eu + 2 * ULP * (v * u).abs(), True, "h")
+    last = bbs.MXFP8Tensor(c[0].codes[-48:], c[0].scales[-48:], 48, F)
+    checkpoint_within(last, g, Eg, "g8")
+
+
 def test_streams_and_graphs(bbs):
     """The operators on a side stream, and captured together into a graph that
     is replayed with new inputs, give the eager bits."""
