@@ -36,20 +36,10 @@ __device__ __forceinline__ uint32_t checkpoint16(const f32x16 &v, uint32_t (&w)[
     return byte;
 }
 
-// Row m, first column n = block + 4 (l / 32) of an M x N checkpoint; N is a
-// multiple of 32, so a block is wholly in or out.
-__device__ __forceinline__ void store_checkpoint(const uint32_t (&w)[4], uint32_t byte,
-                                                 uint8_t *codes, uint8_t *scales, int64_t N,
-                                                 int64_t m, int64_t n, int lane) {
-    if (n >= N) return;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint32_t *>(codes + m * N + n + 8 * q) = w[q];
-    if (lane < 32) scales[m * (N / 32) + n / 32] = (uint8_t)byte;
-}
-
-// The same with the words exchanged between lanes l and l ^ 32 first: lane half
-// h then holds the block's columns 16 h .. 16 h + 15 and stores them at once.
-// n: the block's first column.  Every lane of the wave takes part.
+// Into row m, block at column n of an M x N checkpoint, with the words exchanged
+// between lanes l and l ^ 32 first: lane half h then holds the block's columns
+// 16 h .. 16 h + 15 and stores them at once.  N is a multiple of 32, so a block
+// is wholly in or out.  Every lane of the wave takes part.
 __device__ __forceinline__ void store_checkpoint16(const uint32_t (&w)[4], uint32_t byte, uint8_t *codes,
                                                    uint8_t *scales, int64_t N, bool row_in, int64_t m,
                                                    int64_t n, int half) {

@@ -308,7 +308,7 @@ struct TilePlace {
 
 // TAIL: as for the few-token step, the lane's two 16-value halves are loaded
 // from inside K and cleared where they lie past it.
-template <int SC, int NM, int NR, bool TAIL>
+template <int SC, int NM, int NR, bool TAIL, bool SCALES = true>
 __device__ __forceinline__ void load_weights(TileWeights<NM, NR> &tw, const GemvParams &p,
                                              const TilePlace<NR> &pl, int64_t n0, int64_t k0) {
     const int g = (threadIdx.x & 63) >> 4;
@@ -326,7 +326,7 @@ __device__ __forceinline__ void load_weights(TileWeights<NM, NR> &tw, const Gemv
         for (int r = 0; r < NR; ++r) {
             if (!TAIL) {
                 tw.c[w][r] = *reinterpret_cast<const uint4 *>(cb + pl.code[r]);
-                tw.s[w][r] = SC == kRows32 ? load_bytes<1>(sb + pl.scale[r]) : load_bytes<2>(sb + pl.scale[r]);
+                if (SCALES) tw.s[w][r] = load_bytes<SC == kRows32 ? 1 : 2>(sb + pl.scale[r]);
             } else {
                 const uint8_t *row = cb + pl.code[r] - 16 * g;
                 const uint2 c0 = *reinterpret_cast<const uint2 *>(row + 8 * h0);
@@ -403,9 +403,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
 
     const int64_t full = p.K / kTileK;
     TileWeights<NM, NR> tw;
-    for (int64_t at = wave; at < full; at += nw) {
-        const int64_t k0 = at * kTileK;
-        load_weights<SC, NM, NR, false>(tw, p, pl, n0, k0);
+    const auto step = [&](int64_t k0) {
         // the wave's reads of the step before are done
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
@@ -414,6 +412,46 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
         tile_products<SC, NM, NT, NR>(acc, tw, [&](int t, int j) {
             return *reinterpret_cast<const bf16x8 *>(xl + (16 * t + i) * 256 + 16 * ((4 * g + j) ^ i));
         });
+    };
+    int64_t at = 0;                                       // steps done by all waves
+    // Runs of steps of one wave, whose row scales come with one load of 16
+    // bytes a row: a load for every step touches the same lines again for a
+    // byte or two a lane (48 tokens, MXFP4 14336 x 4096: 16.6 us against 19.0;
+    // gated, 16 tokens, NVFP4: 20.8 against 22.8).  NVFP4's runs are half as
+    // long and lose elsewhere (64 tokens, 4096 x 14336: 30.6 against 29.4; 16
+    // tokens, 14336 x 4096: 13.1 against 12.8; gated, 40 tokens, 4096 x 8192:
+    // 22.3 against 20.9), and rows that do not begin at four bytes make such
+    // loads slow (gated, 13 tokens, 1552 x 4112: 9.0 against 7.0).
+    constexpr int kRun = SC == kRows32 ? 4 : 2;
+    if constexpr (SC == kRows32 || (SC == kRows16 && NM == 2 && NR == 2)) {
+        const int64_t runs = p.K % (SC == kRows32 ? 128 : 64) ? 0 : full;
+        for (; at + kRun * nw <= runs; at += kRun * nw) {
+            const int64_t k0 = (at + kRun * wave) * kTileK;
+            uint4 sv[NM][NR];
+#pragma unroll
+            for (int w = 0; w < NM; ++w)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const uint8_t *row = (w ? p.u : p.w).scales + (n0 * p.K + k0) / (SC == kRows32 ? 32 : 16) +
+                                         (pl.scale[r] - (SC == kRows32 ? g : 2 * g));
+                    __builtin_memcpy(&sv[w][r], row, 16);
+                }
+#pragma unroll
+            for (int q = 0; q < kRun; ++q) {
+                load_weights<SC, NM, NR, false, false>(tw, p, pl, n0, k0 + q * kTileK);
+#pragma unroll
+                for (int w = 0; w < NM; ++w)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        if (SC == kRows32) tw.s[w][r] = word(sv[w][r], q) >> (8 * g) & 0xff;
+                        else tw.s[w][r] = word(sv[w][r], 2 * q + (g >> 1)) >> (16 * (g & 1)) & 0xffff;
+                step(k0 + q * kTileK);
+            }
+        }
+    }
+    for (at += wave; at < full; at += nw) {
+        load_weights<SC, NM, NR, false>(tw, p, pl, n0, at * kTileK);
+        step(at * kTileK);
     }
     if (full % nw == wave && p.K % kTileK) {
         const int64_t k0 = full * kTileK;

@@ -137,6 +137,19 @@ def test_gated_gemv(bbs, T, N, K, fmt, tile2d, bf16, pad, act):
     check(full, T, N, bf16, act64(act, g) * u, gated_bound(act, g, u, Eg, Eu), "h")
 
 
+# Runs of steps with joint scale loads: whole runs only, runs with single steps
+# and a partial step behind them, rows whose scales begin at any byte.
+@pytest.mark.parametrize("T,N,K", [(9, 8208, 4096), (33, 80, 8192 + 384 + 64), (5, 8195, 4096 + 96), (20, 16, 12288)])
+def test_gemv_runs(bbs, T, N, K):
+    test_gemv(bbs, T, N, K, "mxfp4", False, False, 0)
+
+
+@pytest.mark.parametrize("fmt,T,N,K", [("nvfp4", 7, 8208, 2240), ("nvfp4", 18, 48, 4096 + 192), ("nvfp4", 6, 64, 2048),
+                                       ("mxfp4", 6, 8200, 4096 + 160), ("mxfp4", 50, 33, 8192)])
+def test_gated_gemv_runs(bbs, fmt, T, N, K):
+    test_gated_gemv(bbs, T, N, K, fmt, False, False, 0, "silu")
+
+
 def identity16(bbs):
     """The 16 x 16 identity as an NVFP4 tensor (code 1.0, scale 1)."""
     codes = np.zeros((16, 8), np.uint8)
