@@ -78,14 +78,13 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t byte, float (&v)[4]
     v[3] = hi[1];
 }
 
-// Four consecutive columns of one row through the gated activation's
-// backward pass: dh times u act'(g) and act(g), stored to dgate and dup.
-// g_word, u_word: their checkpoint codes; g_byte, u_byte: the block scales.
-template <int ACT, bool BF16_OUT, typename Acc>
-__device__ __forceinline__ void gated_bwd4(const GatedBwdParams &p, int64_t m, int64_t n, const Acc &dh,
-                                           uint32_t g_word, uint32_t g_byte, uint32_t u_word,
-                                           uint32_t u_byte) {
-    float g[4], u[4], dg[4], du[4];
+// Four consecutive columns of one row through the gated activation's backward
+// pass: dgate = dh u act'(g), dup = dh act(g).  g_word, u_word: their
+// checkpoint codes; g_byte, u_byte: the block scales.
+template <int ACT, bool BF16_OUT>
+__device__ __forceinline__ void gated_grad4(const float (&dh)[4], uint32_t g_word, uint32_t g_byte,
+                                            uint32_t u_word, uint32_t u_byte, float (&dg)[4], float (&du)[4]) {
+    float g[4], u[4];
     decode4(g_word, g_byte, g);
     decode4(u_word, u_byte, u);
 #pragma unroll
@@ -95,8 +94,18 @@ __device__ __forceinline__ void gated_bwd4(const GatedBwdParams &p, int64_t m, i
         dg[e] = dh[e] * u[e] * slope;
         du[e] = dh[e] * a;
     }
-    store4<BF16_OUT>(p.mm.c, m * p.mm.ldc + n, dg[0], dg[1], dg[2], dg[3]);
-    store4<BF16_OUT>(p.du, m * p.mm.ldc + n, du[0], du[1], du[2], du[3]);
+}
+
+// Eight consecutive outputs.
+template <bool BF16_OUT>
+__device__ __forceinline__ void store8(void *base, int64_t at, const float (&a)[4], const float (&b)[4]) {
+    if (BF16_OUT) {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at) =
+            make_uint4(pk_bf16(a[0], a[1]), pk_bf16(a[2], a[3]), pk_bf16(b[0], b[1]), pk_bf16(b[2], b[3]));
+    } else {
+        store4<false>(base, at, a[0], a[1], a[2], a[3]);
+        store4<false>(base, at + 4, b[0], b[1], b[2], b[3]);
+    }
 }
 
 }  // namespace bbs

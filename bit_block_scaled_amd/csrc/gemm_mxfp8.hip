@@ -648,10 +648,15 @@ struct GatedBwd {
                 const int at = r * mx::BK + 16 * mx::swz(r, jj) + 4 * (lane >> 4);
                 const uint32_t gw = *reinterpret_cast<const uint32_t *>(gp + at);
                 const uint32_t uw = *reinterpret_cast<const uint32_t *>(up + at);
-                if (full || (m < M && nl + jj * 16 < N))
-                    gated_bwd4<ACT, BF16_OUT>(p, m, nl + jj * 16, acc[i][jj], gw,
-                                              (gs[i] >> (8 * (jj >> 1))) & 0xFFu, uw,
-                                              (us[i] >> (8 * (jj >> 1))) & 0xFFu);
+                if (full || (m < M && nl + jj * 16 < N)) {
+                    const float dh[4] = {acc[i][jj][0], acc[i][jj][1], acc[i][jj][2], acc[i][jj][3]};
+                    float dg[4], du[4];
+                    gated_grad4<ACT, BF16_OUT>(dh, gw, (gs[i] >> (8 * (jj >> 1))) & 0xFFu, uw,
+                                               (us[i] >> (8 * (jj >> 1))) & 0xFFu, dg, du);
+                    const int64_t to = m * p.mm.ldc + nl + jj * 16;
+                    store4<BF16_OUT>(p.mm.c, to, dg[0], dg[1], dg[2], dg[3]);
+                    store4<BF16_OUT>(p.du, to, du[0], du[1], du[2], du[3]);
+                }
             }
         }
     }
