@@ -536,14 +536,17 @@ hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipSt
 //   rows x F x K        large    128     128, 2 groups   64      64, 2 groups
 //   256 x 4096 x 4096   64 us    41 us   39 us           22 us   22 us    (256 tiles of 64)
 //   512 x 4096 x 2048   43 us    27 us   26 us           20 us   23 us    (512 of 64)
-//   1024 x 4096 x 4096  66 us    46 us   43 us           66 us   70 us    (256 of 128)
-//   2048 x 4096 x 1536  41 us    36 us   43 us           48 us   70 us    (512 of 128)
-//   512 x 14336 x 4096  78 us    86 us   98 us          136 us  153 us    (448 of 128)
-// The last two differ in K: the large tile spends about 25 us beside its
-// slabs, two small ones on a CU about 7 us, but more on each slab.  Where K is
-// no multiple of 128 the large tile's rows lie across cache lines, and it
-// wins later (4096 x 4096 x 4000: 140 us against 176; 1536 x 6016 x 2016, 564
-// tiles of 128: 78 against 66).
+//   1024 x 4096 x 4096  66 us    46 us   39 us           66 us   70 us    (256 of 128)
+//   2048 x 4096 x 1536  41 us    30 us   43 us           48 us   70 us    (512 of 128)
+//   512 x 14336 x 4096  71 us    57 us   98 us          136 us  153 us    (448 of 128)
+//   1024 x 10240 x 1536 43 us    41 us                                    (640 of 128)
+//   1024 x 10240 x 4096 70 us    87 us                                    (640 of 128)
+//   4096 x 8192 x 2048  134 us   145 us                                   (2048 of 128)
+// Two small tiles share a CU and one's epilogue runs under the other's slabs,
+// so they win as long as one round of them does the work, and with few slabs
+// a tile also beyond; on each slab the large tile spends less.  The same holds
+// where K is no multiple of 128 (1024 x 10240: 50 and 44 us with K 1504, 89
+// and 105 with 4064).
 hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hipStream_t s) {
     const Mx8GemmParams &mm = p.mm;
     const int64_t lim = (int64_t)1 << 24;          // the large tiles' row offsets are 32 bits wide
@@ -551,7 +554,7 @@ hipError_t launch_gated_bwd(const GatedBwdParams &p, int act, bool bf16_out, hip
     if (t64 <= cus) return bwd<64, 3, 2>(p, act, bf16_out, s);
     if (t64 <= 2 * cus) return bwd<64, 3, 1>(p, act, bf16_out, s);
     if (t128 <= cus) return bwd<128, 2, 2>(p, act, bf16_out, s);
-    const bool large = mm.K % 128 == 0 ? t128 > 2 * cus || mm.K > 2048 : t128 > 3 * cus;
+    const bool large = t128 > 2 * cus && mm.K >= 2048;
     if (large && mm.K < lim && mm.N < lim) return launch_gated_bwd_big(p, act, bf16_out, s);
     return bwd<128, 2, 1>(p, act, bf16_out, s);
 }

@@ -158,9 +158,8 @@ __device__ __forceinline__ void issue(Stage<FP4, ANYK> &st, const Plan &pl, int6
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         const int seg = (w * 8 + q) * 1024;
-        const uint8_t *a = pl.a_base + k0 + pl.a_off[q], *b = pl.b_base + k0 + pl.b_off[q];
-        copy_lds16(ANYK ? lesser(a, ends.a) : a, st.a + seg);
-        copy_lds16(ANYK ? lesser(b, ends.b) : b, st.b + seg);
+        copy_lds16(pl.a_base + k0 + pl.a_off[q], st.a + seg);
+        copy_lds16(pl.b_base + k0 + pl.b_off[q], st.b + seg);
     }
     issue_scales(st, pl, s, ends);
 }
@@ -200,10 +199,8 @@ constexpr int kIssued8 = 18;
 // they get most of two slabs to land, where copying into the other stage of a
 // two-stage ring gives them one.  kn: byte offset of the copied codes.  ANYK:
 // shift holds the byte shifts of the lane's A and B scale words (the rows rl +
-// 16 k of a side share theirs), keep clears the scales of blocks past K, and
-// LAST says that slab sn is the last one, whose copies must stay inside the
-// operands.
-template <bool ANYK = false, bool LAST = false>
+// 16 k of a side share theirs), and keep clears the scales of blocks past K.
+template <bool ANYK = false>
 __device__ __forceinline__ void compute_held(Stage<false, ANYK> &st, f32x4 (&acc)[8][8], int wm,
                                              int wn, int lane, const Plan &pl, int64_t sn,
                                              int64_t kn, const Ends &ends = {}, uint2 shift = {},
@@ -264,9 +261,8 @@ __device__ __forceinline__ void compute_held(Stage<false, ANYK> &st, f32x4 (&acc
             if (k == 6 || (k == 7 && (e & 1))) {
                 if (c < 16) {
                     const int q = c >> 1;
-                    const uint8_t *src = (c & 1 ? pl.b_base + pl.b_off[q] : pl.a_base + pl.a_off[q]) + kn;
-                    if (LAST) src = lesser(src, c & 1 ? ends.b : ends.a);
-                    copy_lds16(src, (c & 1 ? st.b : st.a) + (w * 8 + q) * 1024);
+                    copy_lds16((c & 1 ? pl.b_base + pl.b_off[q] : pl.a_base + pl.a_off[q]) + kn,
+                               (c & 1 ? st.b : st.a) + (w * 8 + q) * 1024);
                 } else if (c == 16) {
                     issue_scales(st, pl, sn, ends);
                 }
@@ -277,14 +273,12 @@ __device__ __forceinline__ void compute_held(Stage<false, ANYK> &st, f32x4 (&acc
     }
 }
 
-// A plan whose code copies bring a 256 x 256 byte tile of an M x N byte matrix
-// into a stage instead of a slab: columns 0-127 of the tile to the A side,
-// 128-255 to the B side, each row's chunks swizzled as a slab's.  Rows and
-// columns past the matrix are clamped: they are never used.  The scale copies
-// stay the slab's.
-__device__ __forceinline__ Plan byte_tile_plan(const Plan &slab, const uint8_t *x, int64_t M, int64_t N,
+// Points a plan's code copies at a 256 x 256 byte tile of an M x N byte matrix
+// instead of a slab: columns 0-127 of the tile to the A side, 128-255 to the B
+// side, each row's chunks swizzled as a slab's.  Rows and columns past the
+// matrix are clamped: they are never used.  The scale copies stay the slabs'.
+__device__ __forceinline__ void byte_tile_plan(Plan &pl, const uint8_t *x, int64_t M, int64_t N,
                                                int64_t m0, int64_t n0) {
-    Plan pl = slab;
     const int t = threadIdx.x, lane = t & 63, w = t >> 6;
     pl.a_base = pl.b_base = x + m0 * N + n0;
 #pragma unroll
@@ -295,7 +289,17 @@ __device__ __forceinline__ Plan byte_tile_plan(const Plan &slab, const uint8_t *
         pl.a_off[q] = (uint32_t)(at + min((int64_t)16 * c, N - 16 - n0));
         pl.b_off[q] = (uint32_t)(at + min((int64_t)128 + 16 * c, N - 16 - n0));
     }
-    return pl;
+}
+
+// Holds the code copies of a slab at byte kn inside the operands (the last
+// slab, where it is partial).
+__device__ __forceinline__ void clamp_codes(Plan &pl, const Ends &ends, int64_t kn) {
+    const int64_t a = ends.a - (pl.a_base + kn), b = ends.b - (pl.b_base + kn);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        pl.a_off[q] = (uint32_t)min((int64_t)pl.a_off[q], a);
+        pl.b_off[q] = (uint32_t)min((int64_t)pl.b_off[q], b);
+    }
 }
 
 // FP4 slabs on v_mfma_scale_f32_32x32x64_f8f6f4, the full-rate form for
@@ -456,42 +460,38 @@ __device__ __forceinline__ void mx_gemm_big(const Mx8GemmParams &p, uint8_t *sme
             }
             __syncthreads();
         };
-        auto tile = [&](const uint8_t *x) { return mx::byte_tile_plan(pl, x, p.M, p.N, m0, n0); };
-        mx::issue(sm.st[0], pl, 0, ends);
-        if (nslab > 1) {
-            mx::issue(sm.st[1], pl, 1, ends);
-        } else {
-            const mx::Plan tp = tile(finish.tile0());
-            mx::Ends open = ends;                     // the tile's own clamps hold for its code copies
-            open.a = open.b = reinterpret_cast<const uint8_t *>(~(uintptr_t)0);
-            mx::issue(sm.st[1], tp, 0, open);
-        }
+        // The copies in the loop's shadow: slabs two ahead, then tile 0, then
+        // tile 1.  The plan changes in place (uniform branches taken once), so
+        // the loop holds one copy of the slab's instructions, and all products
+        // belong to it: after the loop the compiler would move them into the
+        // epilogue's blocks for rows inside C, where the lanes of other rows no
+        // longer prepare their share of the operands, and behind a branch of
+        // the loop they would all run at its end.
+        mx::Plan cur = pl;
+        const auto point_at = [&](int64_t sn) __attribute__((always_inline)) {
+            if (sn >= nslab) mx::byte_tile_plan(cur, sn == nslab ? finish.tile0() : finish.tile1(), p.M, p.N, m0, n0);
+            else if (tail && sn == nslab - 1) mx::clamp_codes(cur, ends, sn * mx::BK);
+            return sn < nslab ? sn : 0;               // beside a tile's codes the scales of slab 0, unused
+        };
+        int64_t sn = point_at(0);
+        mx::issue(sm.st[0], cur, sn, ends);
+        sn = point_at(1);
+        mx::issue(sm.st[1], cur, sn, ends);
         mx::wait_vmcnt<kIssued>();
         __syncthreads();
-        __builtin_amdgcn_s_waitcnt(0xC07F);           // no scalar load in flight into the loop
-        // slabs 0 .. nslab - 3 copy the slab two ahead; with ANYK the last of
-        // these copies is the one that may end inside a slab
-        const int64_t plain_end = ANYK ? nslab - 3 : nslab - 2;
-        int64_t s = 0;
-        for (; s < plain_end; ++s) {
-            mx::compute_held<ANYK>(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK, ends, shift);
+        uint32_t keep = ~0u;
+        for (int64_t s = 0; s < nslab; ++s) {
+            sn = s + 2;
+            if (sn >= nslab - 1) sn = point_at(sn);
+            if (tail && s == nslab - 1) {
+                clear_past(sm.st[s & 1]);
+                keep = (1u << (8 * (tail / 32))) - 1;
+            }
+            __builtin_amdgcn_s_waitcnt(0xC07F);       // no scalar load in flight into the slab
+            mx::compute_held<ANYK>(sm.st[s & 1], acc, wm, wn, lane, cur, sn, sn * mx::BK, ends, shift, keep);
             mx::wait_vmcnt<kIssued>();
             __syncthreads();
         }
-        if (ANYK && nslab > 2) {
-            mx::compute_held<ANYK, true>(sm.st[s & 1], acc, wm, wn, lane, pl, s + 2, (s + 2) * mx::BK, ends, shift);
-            mx::wait_vmcnt<kIssued>();
-            __syncthreads();
-        }
-        if (nslab > 1) {
-            mx::compute_held<ANYK>(sm.st[nslab & 1], acc, wm, wn, lane, tile(finish.tile0()), 0, 0, ends, shift);
-            mx::wait_vmcnt<kIssued>();
-            __syncthreads();
-        }
-        if (tail) clear_past(sm.st[(nslab - 1) & 1]);
-        const uint32_t keep = tail ? (1u << (8 * (tail / 32))) - 1 : ~0u;
-        mx::compute_held<ANYK>(sm.st[(nslab - 1) & 1], acc, wm, wn, lane, tile(finish.tile1()), 0, 0, ends, shift,
-                               keep);
         finish(sm.st[nslab & 1].a, sm.st[(nslab - 1) & 1].a, acc, m0, n0, wm, wn, lane);
     } else if constexpr (!FP4) {
         // Slab s lives in stage s % 2 and is copied while slab s - 2 is

@@ -589,6 +589,17 @@ def test_gated_bwd_large(bbs, M, F, K, act, bf16, shift):
     within(d[:, F:], dh * a, (dh.abs() + Ed) * ea + a.abs() * Ed + 2 * ULP * (dh * a).abs(), bf16, "dU")
 
 
+# K from which the large tiles serve: whole slabs (odd and even counts) and
+# partial last slabs, scales at any byte, tiles partly outside dgate.
+@pytest.mark.parametrize("M,F,K,act,bf16,shift", [
+    (2500, 3360, 2048, "silu", True, 0), (2500, 3360, 2176, "gelu", False, 0), (2500, 3360, 2048, "silu", False, 1),
+    (2500, 3360, 2080, "gelu", True, 0), (2500, 3360, 2144, "silu", True, 3), (3000, 4128, 2272, "gelu", False, 2),
+    (300, 27008, 2240, "silu", True, 0), (33000, 288, 2112, "gelu", True, 0)])
+def test_gated_bwd_large_k(bbs, M, F, K, act, bf16, shift):
+    test_gated_bwd_large(bbs, M, F, K, act, bf16, shift)
+
+
+
 def test_nan_rows_do_not_leak(bbs):
     """A NaN code in one row of dY or Wt reaches that row's or column's outputs alone,
     also where K ends inside a slab and a copy runs into the next row."""
