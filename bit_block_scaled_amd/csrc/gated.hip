@@ -80,9 +80,17 @@ struct FwdStage {
     uint32_t sc[3][TM + 2 * kBF];    // the words that hold a row's 8 scale bytes (A rows, then B rows)
 };
 
-// The tile's B row r holds weight row n0 + 32 (r / 64) + r % 32, of the gate
-// matrix where r / 32 is even and of the up matrix where it is odd.
-__device__ __forceinline__ int b_column(int r) { return 32 * (r >> 6) + (r & 31); }
+// The tile's B rows alternate 32 rows of the gate matrix and the same 32 of the
+// up matrix.  The product's blocks give lane half h rows 8 q + 4 h + e of each
+// 32, which hold columns 16 h + 4 q + e of the block: a lane's outputs are then
+// 16 consecutive columns, and its half of a checkpoint's block one store.
+__device__ __forceinline__ int b_column(int r) {
+    return 32 * (r >> 6) + 16 * (r >> 2 & 1) + 4 * (r >> 3 & 3) + (r & 3);
+}
+// Row of the gate matrix' column c (the up matrix' row is 32 further).
+__device__ __forceinline__ int b_row(int c) {
+    return 64 * (c >> 5) + 8 * (c >> 2 & 3) + 4 * (c >> 4 & 1) + (c & 3);
+}
 
 template <int TM, int NS, int G, int ACT, bool BF16_OUT>
 __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_kernel(GatedParams p) {
@@ -199,7 +207,7 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
             // from 8 bytes earlier: move it into place
             const int c = tail / 32;
             const int64_t col = p.N - 1 - n0;
-            const int64_t r = t == 0 ? p.a.rows - 1 - m0 : 64 * (col >> 5) + 32 * (t - 1) + (col & 31);
+            const int64_t r = t == 0 ? p.a.rows - 1 - m0 : b_row((int)min(col, (int64_t)kBF)) + 32 * (t - 1);
             if (last && (t == 0 ? r < TM : t <= 2 && col < kBF)) {
                 uint8_t *piece = (t == 0 ? d.a : d.b) + r * 64 + 16 * big::swz((int)r, c);
                 *reinterpret_cast<uint2 *>(piece) = *reinterpret_cast<const uint2 *>(piece + 8);
@@ -266,7 +274,7 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
     join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[RA * 32]>(acc));
     if (grp) return;
     const float sg = p.b.s_dec[0], su = p.u.s_dec[0];
-    const int64_t nb = n0 + wn * 32, n = nb + 4 * h;       // the block's and the lane's first column
+    const int64_t n = n0 + wn * 32 + 16 * h;               // the lane's first column
 #pragma unroll
     for (int i = 0; i < RA; ++i) {
         const int64_t m = m0 + wm * (TM / 2) + i * 32 + rl;
@@ -274,21 +282,26 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
         f32x16 g = acc[i][0], u = acc[i][1];
         scale16(g, sa * sg);
         scale16(u, sa * su);
+        const bool in = m < p.M && n < p.N;
         if (p.g_codes) {
-            uint32_t w[4];
-            const uint32_t bg = checkpoint16(g, w);
-            store_checkpoint16(w, bg, p.g_codes, p.g_scales, p.N, m < p.M, m, nb, h);
-            const uint32_t bu = checkpoint16(u, w);
-            store_checkpoint16(w, bu, p.u_codes, p.u_scales, p.N, m < p.M, m, nb, h);
+            uint32_t wg[4], wu[4];
+            const uint32_t bg = checkpoint16(g, wg), bu = checkpoint16(u, wu);
+            if (in) {
+                *reinterpret_cast<uint4 *>(p.g_codes + m * p.N + n) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+                *reinterpret_cast<uint4 *>(p.u_codes + m * p.N + n) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+                if (h == 0) {
+                    p.g_scales[m * (p.N / 32) + n / 32] = (uint8_t)bg;
+                    p.u_scales[m * (p.N / 32) + n / 32] = (uint8_t)bu;
+                }
+            }
         }
-        if (m >= p.M) continue;
+        if (!in) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (n + 8 * q >= p.N) continue;
-            float y[4];
+        for (int q = 0; q < 4; q += 2) {
+            float y[2][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
-            store4<BF16_OUT>(p.h, m * p.ldh + n + 8 * q, y[0], y[1], y[2], y[3]);
+            for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
+            store8<BF16_OUT>(p.h, m * p.ldh + n + 4 * q, y[0], y[1]);
         }
     }
 }
