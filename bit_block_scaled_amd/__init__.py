@@ -366,16 +366,23 @@ def mxfp8_gemm_gated_bwd(dY, Wt, g_ckpt, u_ckpt, dG, dU, dtype, act=ACT_SILU, ld
 def nvfp4_gemv(fmt, x, W, y, y_dtype, ldy=None, stream=None):
     """y = x * W^T for 1 to GEMV_MAX_TOKENS tokens: x BF16 patterns [T, K] (row
     stride x.stride(0)), W an NVFP4Tensor or MXFP4Tensor [N, K] by fmt."""
+    T, ldx = x.shape                # a single row's stride may be anything in PyTorch and is not used
+    if T > 1:
+        ldx = x.stride(0)
+    if ldy is None:
+        ldy = y.stride(0) if T > 1 else y.shape[1]
     wd = W.desc()
-    ldy = y.stride(0) if ldy is None else ldy
-    _check(lib.nvfp4_gemv(fmt, _ptr(x), x.shape[0], x.stride(0), C.byref(wd), _ptr(y), y_dtype, ldy,
-                          _stream(stream)))
+    _check(lib.nvfp4_gemv(fmt, x.data_ptr(), T, ldx, C.byref(wd), y.data_ptr(), y_dtype, ldy, _stream(stream)))
 
 
 def nvfp4_gated_gemv(fmt, x, Wg, Wu, h, h_dtype, act=ACT_SILU, ldh=None, stream=None):
     """h = act(x * Wg^T) * (x * Wu^T) for 1 to GEMV_MAX_TOKENS tokens, operands as
     nvfp4_gemv."""
+    T, ldx = x.shape                # as nvfp4_gemv
+    if T > 1:
+        ldx = x.stride(0)
+    if ldh is None:
+        ldh = h.stride(0) if T > 1 else h.shape[1]
     gd, ud = Wg.desc(), Wu.desc()
-    ldh = h.stride(0) if ldh is None else ldh
-    _check(lib.nvfp4_gated_gemv(fmt, _ptr(x), x.shape[0], x.stride(0), C.byref(gd), C.byref(ud), act,
-                                _ptr(h), h_dtype, ldh, _stream(stream)))
+    _check(lib.nvfp4_gated_gemv(fmt, x.data_ptr(), T, ldx, C.byref(gd), C.byref(ud), act, h.data_ptr(), h_dtype,
+                                ldh, _stream(stream)))

@@ -142,10 +142,7 @@ __device__ __forceinline__ Plan make_plan(const Fp4View &A, const BSide &B, int6
     auto brow = [&](int r) -> int64_t { return min(n0 + B.template row<NJ>(r), n_end - 1); };
     const int pos = swz(lane >> 2, lane & 3);     // (row >> 2) & 3 == (lane >> 4) & 3 here
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int r = (w * 4 + q) * 16 + (lane >> 2);
-        pl.a[q] = A.codes + (int64_t)ar.c[q] * kb + 16 * pos;
-    }
+    for (int q = 0; q < 4; ++q) pl.a[q] = A.codes + (int64_t)ar.c[q] * kb + 16 * pos;
 #pragma unroll
     for (int q = 0; q < NJ; ++q) {
         const int r = (w * NJ + q) * 16 + (lane >> 2);

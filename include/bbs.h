@@ -343,7 +343,8 @@ int grouped_nvfp4_gemm_s2f6(const bbs_fp4 *A, const int32_t *row_index,
  * mxfp8_gemm_gated_bwd: the MXFP8 copies of the FP32 values, M x F (F % 32
  * == 0), rounded to nearest even as the row_mx8 copy of nvfp4_quantize.
  * Products and checkpointed values must be finite.  K % 128 == 0 with 8-byte
- * aligned scales is the fast case.  A may have a decode scale per row.
+ * aligned scales is the fast case of large problems.  A may have a decode
+ * scale per row.
  * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale
  * or with different tile2d. */
 int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act,
@@ -361,7 +362,7 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
  * 16 == 0; they may be the two halves of one M x 2F matrix (ld = 2F), the
  * row operand of the weights' gradient and of the block's input gradient.
  * act as for the forward pass.  K % 128 == 0 with 4-byte aligned scales is
- * the fast case.  Errors: BBS_EINVAL. */
+ * the fast case of large problems.  Errors: BBS_EINVAL. */
 int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8,
                          const bbs_mx8 *u8, int32_t act, void *dG, void *dU, int32_t dtype,
                          int64_t ld, void *stream);
@@ -373,10 +374,10 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
  *      decode scale), fmt == BBS_FMT_MXFP4: a const bbs_mx4 *.
  * x is tokens x K (BF16 patterns, row stride ldx elements, ldx % 8 == 0,
  * 16-byte aligned), W is N x K, y is tokens x N with row stride ldy (>= N)
- * elements.  The order of the sums depends on the sizes alone, so the same
- * call gives the same bits.  Errors: BBS_EINVAL; BBS_ENOTSUP for a weight
- * with a per-row decode scale, or with more than 2^31 - 1 rows or 2^26
- * columns. */
+ * elements.  A weight (code times scale) must be below 2^128.  The order of the sums
+ * depends on the sizes alone, so the same call gives the same bits.
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for a weight with a per-row decode scale,
+ * or with more than 2^31 - 1 rows or 2^26 columns. */
 int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
                void *y, int32_t y_dtype, int64_t ldy, void *stream);
 

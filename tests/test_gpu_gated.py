@@ -218,6 +218,47 @@ def test_gemv_extreme_scales(bbs):
     check(fullm, T, N, False, *product(xv, m.dequant_f64()), "mxfp4")
 
 
+@pytest.mark.parametrize("T", [1, 2, 4, 6, 48])
+def test_gemv_ends_of_the_exponents(bbs, T):
+    """MXFP4 block scales from 2^-127 (whose products with codes are BF16
+    subnormals) to 2^125, and subnormal activations."""
+    announce(f"gemv ends of the exponents {T}")
+    N, K = 40, 288
+    rng = np.random.default_rng(6)
+    codes = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    for bytes_, shift in (((0, 1, 2), 60), ((250, 251, 252), -60)):
+        ms = rng.choice(np.array(bytes_, np.uint8), (N, K // 32))
+        xb = synth.normal(T, K, 61, 2.0 ** shift)
+        W = bbs.MXFP4Tensor(to_dev(codes), to_dev(ms), N, K)
+        full, y = output(T, N, False)
+        bbs.nvfp4_gemv(2, to_dev(xb), W, y, 0)
+        torch.cuda.synchronize()
+        check(full, T, N, False, *product(bf16_bits_to_f64(xb), O.MXFP4(codes, ms, N, K).dequant_f64()), "scales")
+    ms = rng.choice(np.array([160, 161, 163], np.uint8), (N, K // 32))
+    xb = rng.integers(0, 128, (T, K)).astype(np.uint16) | (rng.integers(0, 2, (T, K)) << 15).astype(np.uint16)
+    full, y = output(T, N, False)
+    bbs.nvfp4_gemv(2, to_dev(xb), bbs.MXFP4Tensor(to_dev(codes), to_dev(ms), N, K), y, 0)
+    torch.cuda.synchronize()
+    check(full, T, N, False, *product(bf16_bits_to_f64(xb), O.MXFP4(codes, ms, N, K).dequant_f64()), "activations")
+
+
+def test_gemv_single_row_strides(bbs):
+    """One token whose row stride is not a row's width (PyTorch allows any there)."""
+    announce("gemv: strides of a single row")
+    N, K = 48, 64
+    W, w = weight(bbs, "nvfp4", N, K, 51)
+    x, xv = tokens(1, K, 52)
+    odd = x.as_strided((1, K), (1, 1))
+    for y in (torch.zeros((N, 1), device=dev()).t(), torch.zeros((1, N), device=dev()).as_strided((1, N), (5, 1))):
+        bbs.nvfp4_gemv(0, odd, W, y, 0)
+        h = torch.zeros_like(y).as_strided((1, N), (3, 1))
+        bbs.nvfp4_gated_gemv(0, odd, W, W, h, 0)
+        torch.cuda.synchronize()
+        ref, E = product(xv, w)
+        assert np.all(np.abs(host(y).astype(np.float64) - ref) <= E)
+        assert np.all(np.abs(host(h) - act64("silu", ref) * ref) <= gated_bound("silu", ref, ref, E, E))
+
+
 def test_gemv_offsets_beyond_32_bits(bbs):
     """Code bytes past 4 GiB: the last rows of a tall matrix."""
     announce("gemv past 4 GiB")
@@ -554,7 +595,30 @@ def test_gated_gemm_large(bbs, M, F, K, tile2d, act, bf16, ckpt, shift):
         checkpoint_within(c[1], u, Eu, "u8")
 
 
-# 540 tiles of 128 x 128 take the large tiles for K % 128 == 0, 792 for any K
+@pytest.mark.parametrize("M,F,K,ckpt", [(1040, 2080, 256, True), (2064, 2000, 400, False), (272, 1568, 1184, True),
+                                        (528, 2736, 1552, False), (64, 320, 128, True)])
+@pytest.mark.parametrize("scales", ["rows", "tiles"])
+def test_gated_gemm_scales_of_a(bbs, M, F, K, ckpt, scales):
+    """A with a decode scale per row, and with 16x16 block scales, at every tile size."""
+    announce(f"gated gemm {M} x {F} x {K} ckpt={ckpt} A scales: {scales}")
+    A = random_nv(bbs, M, K, scales == "tiles", 1)
+    if scales == "rows":
+        d = (1.0 + torch.arange(M, device=dev()) % 7) * 0.25 / K ** 0.5
+        A = bbs.NVFP4Tensor(A.codes, A.scales, d.float(), M, K, False, sdec_per_row=True)
+    Wg, Wu = random_nv(bbs, F, K, True, 2), random_nv(bbs, F, K, True, 3)
+    h = torch.full((M, F), 7.0, dtype=torch.float32, device=dev())
+    c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) if ckpt else None for _ in range(2)]
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, 0, g_ckpt=c[0], u_ckpt=c[1])
+    a = nv64(A)
+    (g, Eg), (u, Eu) = product_t(a, nv64(Wg)), product_t(a, nv64(Wu))
+    v, _, ea, _ = act_t("silu", g)
+    within(h, v * u, (u.abs() + Eu) * (1.13 * Eg + ea) + v.abs() * Eu + 2 * ULP * (v * u).abs(), False, "h")
+    if ckpt:
+        checkpoint_within(c[0], g, Eg, "g8")
+        checkpoint_within(c[1], u, Eu, "u8")
+
+
+# one to many slabs of many tiles, whole and partial
 LARGE_BWD = [
     (2500, 3360, 128, "silu", True, 0),
     (2500, 3360, 256, "gelu", False, 0),
@@ -682,3 +746,41 @@ def test_streams_and_graphs(bbs):
         calls(eager)
         torch.cuda.synchronize()
         assert same(eager, cap), r
+
+
+def test_calls_at_once(bbs):
+    """The same calls on two streams at once, with operands and outputs of their
+    own: what each gives alone."""
+    announce("gated operators: two streams at once")
+    M, F, K = 512, 1024, 1024
+
+    def problem(seed):
+        A = random_nv(bbs, M, K, False, seed)
+        Wg, Wu = random_nv(bbs, F, K, True, seed + 1), random_nv(bbs, F, K, True, seed + 2)
+        dY, Wt = random_mx(bbs, M, K, seed + 3), random_mx(bbs, F, K, seed + 4)
+        x = torch.randn((20, K), device=dev(), generator=torch.Generator(device=dev()).manual_seed(seed)).bfloat16()
+        return A, Wg, Wu, dY, Wt, x
+
+    def run(q):
+        A, Wg, Wu, dY, Wt, x = q
+        h, d = (torch.empty((M, n), dtype=torch.bfloat16, device=dev()) for n in (F, 2 * F))
+        v, y = (torch.empty((20, F), dtype=torch.float32, device=dev()) for _ in range(2))
+        c = [bbs.MXFP8Tensor.empty(M, F, device=dev()) for _ in range(2)]
+        for _ in range(8):
+            bbs.nvfp4_gated_gemm(A, Wg, Wu, h, 1, g_ckpt=c[0], u_ckpt=c[1])
+            bbs.mxfp8_gemm_gated_bwd(dY, Wt, *c, d[:, :F], d[:, F:], 1)
+            bbs.nvfp4_gated_gemv(0, x, Wg, Wu, v, 0)
+            bbs.nvfp4_gemv(0, x, Wu, y, 0)
+        return h, d, v, y
+
+    probs = problem(10), problem(20)
+    alone = [run(q) for q in probs]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    both = []
+    for s, q in zip(streams, probs):
+        with torch.cuda.stream(s):
+            both.append(run(q))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -152,6 +152,64 @@ def test_inference(L, T):
     assert err <= (4 * 2.0 ** -9 if T <= 64 else 0.4)
 
 
+def test_block_and_inference_in_a_graph(L):
+    """Forward and backward passes of one training step, and the inference form
+    with few and with many tokens, captured and replayed: the eager bits, with
+    other eager work between the replays."""
+    announce("QGatedMLP captured")
+    M, K, F = 96, 256, 288
+    b, x, dy, _ = _block(L, M, K, F, "silu")
+    inf = b.inference()
+    xs = [x.detach().reshape(-1, K)[:T].clone() for T in (7, 80)]
+
+    def run(out):
+        with torch.no_grad():
+            out["inf"] = [inf(v) for v in xs]
+        leaves = [t.detach().requires_grad_() for t in (x, b.w_gate_up, b.w_down)]
+        y = L.QGatedMLPFn.apply(*leaves, 0, SEED, 3, SIGNS)
+        out["train"] = [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+
+    eager, cap = {}, {}
+    run(eager)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run({})
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(cap)
+    for r in range(4):
+        with torch.no_grad():
+            x.copy_(torch.roll(x, 1, -1))
+            for v in xs:
+                v.copy_(torch.roll(v, 3, -1))
+        graph.replay()
+        run(eager)
+        torch.cuda.synchronize()
+        for k in eager:
+            assert all(torch.equal(p, q) for p, q in zip(eager[k], cap[k])), (r, k)
+
+
+def test_block_with_an_expanded_gradient_and_a_padded_input(L):
+    """dy of one element (y.sum()), x a slice of a wider tensor: the bits of the dense tensors."""
+    announce("QGatedMLP strides")
+    M, K, F = 64, 128, 96
+    got = []
+    for dense in (True, False):
+        b, x, _, _ = _block(L, M, K, F, "gelu")
+        wide = torch.zeros((*x.shape[:-1], K + 16), dtype=x.dtype, device=x.device)
+        wide[..., :K] = x.detach()
+        xi = x.detach().clone().requires_grad_() if dense else wide[..., :K].requires_grad_()
+        y = b(xi)
+        one = torch.ones((), dtype=y.dtype, device=y.device).expand(y.shape)
+        y.backward(one.contiguous() if dense else one)
+        got.append((y.detach(), xi.grad, b.w_gate_up.grad, b.w_down.grad))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
 def test_refusals(L):
     with pytest.raises(ValueError):
         L.QGatedMLP(64, 48, device=dev())
