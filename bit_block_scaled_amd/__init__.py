@@ -120,10 +120,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# of a build of PyTorch without GPUs these are missing, and no call gets here
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
         # the handle of torch.cuda.current_stream(), without building the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return stream.cuda_stream
 
 
@@ -371,8 +376,10 @@ def nvfp4_gemv(fmt, x, W, y, y_dtype, ldy=None, stream=None):
         ldx = x.stride(0)
     if ldy is None:
         ldy = y.stride(0) if T > 1 else y.shape[1]
-    wd = W.desc()
-    _check(lib.nvfp4_gemv(fmt, x.data_ptr(), T, ldx, C.byref(wd), y.data_ptr(), y_dtype, ldy, _stream(stream)))
+    status = lib.nvfp4_gemv(fmt, x.data_ptr(), T, ldx, C.byref(W.desc()), y.data_ptr(), y_dtype, ldy,
+                            _stream(stream))
+    if status:
+        _check(status)
 
 
 def nvfp4_gated_gemv(fmt, x, Wg, Wu, h, h_dtype, act=ACT_SILU, ldh=None, stream=None):
@@ -383,6 +390,7 @@ def nvfp4_gated_gemv(fmt, x, Wg, Wu, h, h_dtype, act=ACT_SILU, ldh=None, stream=
         ldx = x.stride(0)
     if ldh is None:
         ldh = h.stride(0) if T > 1 else h.shape[1]
-    gd, ud = Wg.desc(), Wu.desc()
-    _check(lib.nvfp4_gated_gemv(fmt, x.data_ptr(), T, ldx, C.byref(gd), C.byref(ud), act, h.data_ptr(), h_dtype,
-                                ldh, _stream(stream)))
+    status = lib.nvfp4_gated_gemv(fmt, x.data_ptr(), T, ldx, C.byref(Wg.desc()), C.byref(Wu.desc()), act,
+                                  h.data_ptr(), h_dtype, ldh, _stream(stream))
+    if status:
+        _check(status)
