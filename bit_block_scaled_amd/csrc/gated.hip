@@ -72,10 +72,10 @@ __device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, in
 // Forward: TM rows by 64 columns of both products.
 //
 // Bound by the expansion of the codes: a wave's 64 x 64 part (TM 128) expands
-// four fragments for every four matrix instructions, about as many VALU cycles
-// as the matrix instructions take, and with two waves a SIMD in step the two
-// hardly overlap.  528 x 2736 x 1552, BF16: 21.9 us on 215 CUs, of which 2.4 a
-// pair of slabs and 5.7 beside them; 272 x 1568 x 1184 with checkpoints 13.1.
+// four fragments for every four matrix instructions.  528 x 2736 x 1552, BF16:
+// 21.9 us on 215 CUs, 2.4 a pair of slabs and 5.7 beside them (on those CUs
+// VALU is active 70% of the slabs' time, the matrix units 40%, over half of it
+// together); 272 x 1568 x 1184 with checkpoints: 13.1 us.
 // Reading the next slab's codes into registers a step ahead, with a ring one
 // stage deeper, made no difference (22.6), so it is not the copies' latency.
 // ---------------------------------------------------------------------------
