@@ -39,12 +39,14 @@ __device__ __forceinline__ const uint8_t *lesser(const uint8_t *a, const uint8_t
 
 // Tile of workgroup b: workgroup b runs on XCD b % 8, so each XCD is given a
 // contiguous range of tile ids, and ids walk 8 row tiles down before moving
-// along the columns, which keeps operand panels in one XCD's L2.
-__device__ __forceinline__ void tile_of(int64_t tm, int64_t tn, int64_t &mt, int64_t &nt) {
-    const int64_t total = tm * tn, x = blockIdx.x % 8, share = total / 8, extra = total % 8;
-    const int64_t id = x * share + (x < extra ? x : extra) + blockIdx.x / 8;
-    const int64_t g = id / (8 * tn), in = id - g * (8 * tn);
-    const int64_t gm = tm - g * 8 < 8 ? tm - g * 8 : 8;
+// along the columns, which keeps operand panels in one XCD's L2.  In 32 bits
+// (the launch holds the tiles to 2^31 - 1), as 64-bit divisions are long
+// (64 x 512 x 512: 8.3 us against 8.6).
+__device__ __forceinline__ void tile_of(uint32_t tm, uint32_t tn, int64_t &mt, int64_t &nt) {
+    const uint32_t total = tm * tn, x = blockIdx.x % 8, share = total / 8, extra = total % 8;
+    const uint32_t id = x * share + (x < extra ? x : extra) + blockIdx.x / 8;
+    const uint32_t g = id / (8 * tn), in = id - g * (8 * tn);
+    const uint32_t gm = tm - g * 8 < 8 ? tm - g * 8 : 8;
     mt = g * 8 + in % gm;
     nt = in / gm;
 }
@@ -113,7 +115,7 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
     const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int64_t m0, n0;
-    tile_of((p.M + TM - 1) / TM, (p.N + kBF - 1) / kBF, m0, n0);
+    tile_of((uint32_t)((p.M + TM - 1) / TM), (uint32_t)((p.N + kBF - 1) / kBF), m0, n0);
     m0 *= TM;
     n0 *= kBF;
     const int64_t kb = p.K / 2, ks = p.K / 16;
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
     const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = wave >> 1, wn = wave & 1;
     int64_t m0, n0;
-    tile_of((mm.M + T - 1) / T, (mm.N + T - 1) / T, m0, n0);
+    tile_of((uint32_t)((mm.M + T - 1) / T), (uint32_t)((mm.N + T - 1) / T), m0, n0);
     m0 *= T;
     n0 *= T;
     const int64_t nkb = mm.K / 32, nslab = (mm.K + 127) / 128;
