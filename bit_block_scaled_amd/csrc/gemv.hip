@@ -388,6 +388,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * NR);
+    const int t0 = blockIdx.y * (16 * NT);                // the workgroup's first token
     TilePlace<NR> pl;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
 #pragma unroll
     for (int q = 0; q < 4 * NT; ++q) {
         const int t = 4 * q + g;
-        src[q] = p.x + min((int64_t)t, p.T - 1) * p.ldx + 8 * (i ^ (t & 15));
+        src[q] = p.x + min((int64_t)(t0 + t), p.T - 1) * p.ldx + 8 * (i ^ (t & 15));
     }
     f32x4 acc[NM][NR][NT];
 #pragma unroll
@@ -472,7 +473,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
         const int left = (int)(p.K - k0) / 8;             // chunks of a token inside K
         tile_products<SC, NM, NT, NR>(acc, tw, [&](int t, int j) {
             const uint4 v = *reinterpret_cast<const uint4 *>(
-                p.x + min((int64_t)(16 * t + i), p.T - 1) * p.ldx + k0 + 8 * min(4 * g + j, left - 1));
+                p.x + min((int64_t)(t0 + 16 * t + i), p.T - 1) * p.ldx + k0 + 8 * min(4 * g + j, left - 1));
             const bool in = 4 * g + j < left;
             return __builtin_bit_cast(bf16x8, make_uint4(in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0));
         });
@@ -495,7 +496,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
             for (int w = 0; w < NM; ++w) v[w] += part[(s * NM + w) * NO + o];
         // consecutive o: rows 4 g + v of one token
         const int tile = o >> 8, l = (o >> 2) & 63;
-        const int64_t t = (tile % NT) * 16 + (l & 15);
+        const int64_t t = t0 + (tile % NT) * 16 + (l & 15);
         const int64_t n = n0 + (tile / NT) * 16 + (l >> 4) * 4 + (o & 3);
         if (t < p.T && n < p.N) finish<SC, NM>(p, t, n, v);
     }
@@ -520,7 +521,7 @@ template <int SC, int NM, int NT, int NR>
 hipError_t tile(const GemvParams &p, hipStream_t s) {
     const int64_t steps = (p.K + kTileK - 1) / kTileK;
     const int64_t waves = std::min<int64_t>(steps, kTileSplit);
-    const dim3 grid((unsigned)((p.N + 16 * NR - 1) / (16 * NR)));
+    const dim3 grid((unsigned)((p.N + 16 * NR - 1) / (16 * NR)), (unsigned)((p.T + 16 * NT - 1) / (16 * NT)));
     // a wave's activations, then its sums
     constexpr size_t wave_bytes = (size_t)NT * 1024 * (NM * NR > 4 ? NM * NR : 4);
     static const bool attr_set = [] {
@@ -542,14 +543,49 @@ hipError_t few_rows(const GemvParams &p, hipStream_t s) {
     return p.N >= 4096 ? few<SC, NM, TT, 4 / NM>(p, s) : few<SC, NM, TT, 2 / NM>(p, s);
 }
 
-// Row tiles of a workgroup, over both matrices: each re-reads the activations
-// once for all its rows, so four where that leaves about a workgroup a CU (48
-// tokens, MXFP4 14336 x 4096: 16.6 us with 64 rows, 22.5 with 32, 30.8 with
-// 16), and as few as there are below (32 tokens, 4096 x 14336: 16.3 us with 16
-// rows, 18.4 with 32; 64 tokens, 1536 x 4096: 8.2 and 10.5 us).
-template <int SC, int NM, int NT>
-hipError_t tile_rows(const GemvParams &p, hipStream_t s) {
-    return p.N >= 8192 ? tile<SC, NM, NT, 4 / NM>(p, s) : tile<SC, NM, NT, 1>(p, s);
+// Row tiles and token tiles of a workgroup.  Each workgroup reads its tokens'
+// activations once for all its rows and its rows once for all its tokens, and
+// more than one workgroup a CU means a second round or less LDS for each.
+//
+// So as few row tiles as keep the grid within the CUs, four over both matrices
+// at most, and then all the tokens (us, NVFP4, K 4096):
+//   tokens x rows   16 rows   32 rows   64 rows
+//   16 x 4608       9.4       7.9                  (288 tiles of 16)
+//   64 x 5120       18        14.4      15.3       (320)
+//   16 x 8192       9.9       8.5       12.3       (512)
+//   40 x 8192       18        12.9      18.4
+//   48 x 14336                22.8      19.6       (896; MXFP4: 16.6 with 64 rows)
+// With short K and one token tile the second row tile costs more than the
+// second round (16 x 4112 x 1568: 4.2 and 4.5 us; 16 x 6144 x 2048: 6.1 and 5.4).
+//
+// One row tile leaves room for fewer tokens in a workgroup: as many token
+// tiles as keep the grid within the CUs (64 tokens, 1536 x 4096: 6.8 us with
+// two, 9.4 with four, 8.8 with one; 512 x 2048: 4.0 with one, 6.2 with four; 24
+// tokens, 4096 x 4096: 7.2 with two, 9.2 with one).  Where that is all four
+// (for one MXFP4 matrix, whose expansion is cheaper, also three), two of each
+// read fewer activations (64 tokens, 4096 x 14336: 26.8 us against 29.3,
+// MXFP4 20.4 against 26.6; 48 tokens 26.1 against 24.4, MXFP4 19.8 and 22.0).
+template <int SC, int NM>
+hipError_t tile_shape(const GemvParams &p, hipStream_t s) {
+    const int64_t rows = (p.N + 15) / 16, tiles = (p.T + 15) / 16, cus = device_cus(s);
+    if (rows > 2 * cus && NM == 1) {
+        if (tiles == 1) return tile<SC, NM, 1, 4 / NM>(p, s);
+        if (tiles == 2) return tile<SC, NM, 2, 4 / NM>(p, s);
+        if (tiles == 3) return tile<SC, NM, 3, 4 / NM>(p, s);
+        return tile<SC, NM, 4, 4 / NM>(p, s);
+    }
+    if (rows > cus && (rows > 2 * cus || tiles > 1 || p.K >= 2048)) {
+        if (tiles == 1) return tile<SC, NM, 1, 2>(p, s);
+        if (tiles == 2) return tile<SC, NM, 2, 2>(p, s);
+        if (tiles == 3) return tile<SC, NM, 3, 2>(p, s);
+        return tile<SC, NM, 4, 2>(p, s);
+    }
+    int64_t nt = 1;
+    while (nt < tiles && rows * ((tiles + nt - 1) / nt) > cus) ++nt;
+    if (nt == 4 || (SC == kRows32 && NM == 1 && nt == 3)) return tile<SC, NM, 2, 2>(p, s);
+    if (nt == 1) return tile<SC, NM, 1, 1>(p, s);
+    if (nt == 2) return tile<SC, NM, 2, 1>(p, s);
+    return tile<SC, NM, 3, 1>(p, s);
 }
 
 // Up to four tokens take the 4x4x4 form (three, 14336 x 4096: 11.3 us against
@@ -560,10 +596,7 @@ hipError_t run(const GemvParams &p, hipStream_t s) {
     if (p.T == 1) return few_rows<SC, NM, 1>(p, s);
     if (p.T == 2) return few_rows<SC, NM, 2>(p, s);
     if (p.T <= 4) return few_rows<SC, NM, 4>(p, s);
-    if (p.T <= 16) return tile_rows<SC, NM, 1>(p, s);
-    if (p.T <= 32) return tile_rows<SC, NM, 2>(p, s);
-    if (p.T <= 48) return tile_rows<SC, NM, 3>(p, s);
-    return tile_rows<SC, NM, 4>(p, s);
+    return tile_shape<SC, NM>(p, s);
 }
 
 template <int SC>

@@ -150,6 +150,22 @@ def test_gated_gemv_runs(bbs, fmt, T, N, K):
     test_gated_gemv(bbs, T, N, K, fmt, False, False, 0, "silu")
 
 
+# Every count of row and token tiles a workgroup may have, with rows and tokens
+# that fill neither.
+@pytest.mark.parametrize("T,N,K,fmt", [(33, 530, 160, "mxfp4"), (64, 528, 272, "nvfp4"), (20, 1552, 144, "nvfp4"),
+                                       (41, 1550, 160, "mxfp4"), (63, 1536, 144, "nvfp4"), (18, 4096, 144, "nvfp4"),
+                                       (39, 4096, 144, "nvfp4"), (47, 4090, 160, "mxfp4"), (55, 4080, 144, "nvfp4"),
+                                       (9, 4112, 272, "nvfp4"), (9, 4112, 2048, "nvfp4"), (19, 4112, 144, "nvfp4"),
+                                       (48, 8190, 160, "mxfp4"), (64, 8192, 80, "nvfp4"), (15, 8208, 144, "nvfp4"),
+                                       (25, 8200, 160, "mxfp4"), (42, 8208, 80, "nvfp4"), (51, 8208, 144, "nvfp4")])
+@pytest.mark.parametrize("gated", [False, True])
+def test_gemv_tile_shapes(bbs, T, N, K, fmt, gated):
+    if gated:
+        test_gated_gemv(bbs, T, N, K, fmt, False, True, 8, "silu")
+    else:
+        test_gemv(bbs, T, N, K, fmt, False, True, 8)
+
+
 def identity16(bbs):
     """The 16 x 16 identity as an NVFP4 tensor (code 1.0, scale 1)."""
     codes = np.zeros((16, 8), np.uint8)
