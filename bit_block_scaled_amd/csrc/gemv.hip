@@ -580,12 +580,13 @@ hipError_t tile_shape(const GemvParams &p, hipStream_t s) {
         if (tiles == 3) return tile<SC, NM, 3, 2>(p, s);
         return tile<SC, NM, 4, 2>(p, s);
     }
+    constexpr int kMost = SC == kRows32 && NM == 1 ? 2 : 3;
     int64_t nt = 1;
     while (nt < tiles && rows * ((tiles + nt - 1) / nt) > cus) ++nt;
-    if (nt == 4 || (SC == kRows32 && NM == 1 && nt == 3)) return tile<SC, NM, 2, 2>(p, s);
+    if (nt > kMost) return tile<SC, NM, 2, 2>(p, s);
     if (nt == 1) return tile<SC, NM, 1, 1>(p, s);
     if (nt == 2) return tile<SC, NM, 2, 1>(p, s);
-    return tile<SC, NM, 3, 1>(p, s);
+    return tile<SC, NM, kMost, 1>(p, s);
 }
 
 // Up to four tokens take the 4x4x4 form (three, 14336 x 4096: 11.3 us against
