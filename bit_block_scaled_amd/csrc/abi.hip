@@ -769,6 +769,8 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
     if (Wg->sdec_per_row || Wu->sdec_per_row)
         return fail(BBS_ENOTSUP, "weights with a per-row decode scale");
     if (Wg->tile2d != Wu->tile2d) return fail(BBS_ENOTSUP, "Wg and Wu with different tile2d");
+    // row offsets inside a tile are 32 bits wide
+    if (A->cols >= (int64_t)1 << 25) return fail(BBS_ENOTSUP, "2^25 columns or more");
     if ((st = check_rows_out(H, h_dtype, Wg->rows, ldh, "H"))) return st;
     if (!g8 != !u8) return fail(BBS_EINVAL, "g8 and u8 come together");
     bbs::GatedParams p{};
@@ -806,6 +808,7 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
     if ((st = check_mx8(u8, "u8"))) return st;
     if (!act_ok(act)) return fail(BBS_EINVAL, "bad act");
     if (dY->cols != Wt->cols) return fail(BBS_EINVAL, "dY.cols != Wt.cols");
+    if (dY->cols >= (int64_t)1 << 25) return fail(BBS_ENOTSUP, "2^25 columns or more");   // as above
     for (const bbs_mx8 *c : {g8, u8})
         if (c->rows != dY->rows || c->cols != Wt->rows)
             return fail(BBS_EINVAL, "g8 and u8 must be dY.rows x Wt.rows");

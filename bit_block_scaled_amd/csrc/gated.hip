@@ -37,6 +37,20 @@ __device__ __forceinline__ const uint8_t *word_of(const uint8_t *p) {
 }
 __device__ __forceinline__ const uint8_t *lesser(const uint8_t *a, const uint8_t *b) { return a < b ? a : b; }
 
+// copy_lds16 from base + off, base the same for the wave.  A scalar register
+// that a vector instruction wrote may be read by a memory instruction five
+// wait states later, which the compiler does not see to in front of an asm.
+__device__ __forceinline__ void copy_at(const uint8_t *base, uint32_t off, const void *lds) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    const uint64_t sb = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
+                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
+    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(sb), "{m0}"(lds_addr(lds))
+                 : "memory");
+}
+
+// An offset held to at most `last`, which is not negative.
+__device__ __forceinline__ uint32_t held(uint32_t off, int64_t last) { return (uint32_t)min((int64_t)off, last); }
+
 // Tile of workgroup b: workgroup b runs on XCD b % 8, so each XCD is given a
 // contiguous range of tile ids, and ids walk 8 row tiles down before moving
 // along the columns, which keeps operand panels in one XCD's L2.  In 32 bits
@@ -75,11 +89,11 @@ __device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, in
 //
 // Bound by the expansion of the codes: a wave's 64 x 64 part (TM 128) expands
 // four fragments for every four matrix instructions.  528 x 2736 x 1552, BF16:
-// 21.9 us on 215 CUs, 2.4 a pair of slabs and 5.7 beside them (on those CUs
+// 20.9 us on 215 CUs, 2.3 a pair of slabs and 5.5 beside them (on those CUs
 // VALU is active 70% of the slabs' time, the matrix units 40%, over half of it
-// together); 272 x 1568 x 1184 with checkpoints: 13.1 us.
+// together); 272 x 1568 x 1184 with checkpoints: 12.5 us.
 // Reading the next slab's codes into registers a step ahead, with a ring one
-// stage deeper, made no difference (22.6), so it is not the copies' latency.
+// stage deeper, made it slower by 5%, so it is not the copies' latency.
 // ---------------------------------------------------------------------------
 constexpr int kBF = 64;
 
@@ -123,21 +137,19 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
     const int tail = (int)(p.K % 128);             // K values of a partial last slab, 0: none
 
     // copy sources (rows past the end are clamped: they feed nothing that is written)
-    const uint8_t *asrc[RA], *bsrc[2], *aend, *bend[2];
+    // as 32-bit offsets (K < 2^25) from the tile's first row, which need no
+    // address arithmetic a copy; a wave copies rows of one weight matrix
+    uint32_t aoff[RA], boff[2];
+    const uint8_t *const abase = p.a.codes + m0 * kb, *const aend = p.a.codes + p.a.rows * kb - 16;
+    const uint8_t *const wcodes = (wave & 1 ? p.u : p.b).codes;
+    const uint8_t *const bbase = wcodes + n0 * kb, *const bend = wcodes + p.N * kb - 16;
     const int pos = big::swz(lane >> 2, lane & 3);
 #pragma unroll
-    for (int q = 0; q < RA; ++q) {
-        const int64_t m = min(m0 + (wave * RA + q) * 16 + (lane >> 2), p.M - 1);
-        asrc[q] = p.a.codes + m * kb + 16 * pos;
-    }
-    aend = p.a.codes + p.a.rows * kb - 16;
+    for (int q = 0; q < RA; ++q)
+        aoff[q] = (uint32_t)(min((int64_t)((wave * RA + q) * 16 + (lane >> 2)), p.M - 1 - m0) * kb) + 16 * pos;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int r = (wave * 2 + q) * 16 + (lane >> 2);
-        const Fp4View &W = ((r >> 5) & 1) ? p.u : p.b;
-        bsrc[q] = W.codes + min(n0 + b_column(r), p.N - 1) * kb + 16 * pos;
-        bend[q] = W.codes + p.N * kb - 16;
-    }
+    for (int q = 0; q < 2; ++q)
+        boff[q] = (uint32_t)(min((int64_t)b_column((wave * 2 + q) * 16 + (lane >> 2)), p.N - 1 - n0) * kb) + 16 * pos;
     // scales: the words of a row's bytes, 64 rows a copy (the waves past the
     // last row repeat the last 64)
     auto scale_row = [&](int r) -> const uint8_t * {
@@ -160,20 +172,30 @@ __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_ke
         ssrc[k] = word_of(scale_row(r));
         slast[k] = word_of(W.scales + (W.tile2d ? rows / 16 : rows) * ks - 1);
     }
+    // the last slab's copies are held inside the operands
     auto issue = [&](int64_t s, int stage) {
         FwdStage<TM> &d = st[stage];
         const int64_t at = s * 64;
-        const bool partial = tail && s == nslab - 1;
+        if (s != nslab - 1) {
 #pragma unroll
-        for (int q = 0; q < RA; ++q)
-            copy_lds16(partial ? lesser(asrc[q] + at, aend) : asrc[q] + at, d.a + (wave * RA + q) * 1024);
+            for (int q = 0; q < RA; ++q) copy_at(abase + at, aoff[q], d.a + (wave * RA + q) * 1024);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-            copy_lds16(partial ? lesser(bsrc[q] + at, bend[q]) : bsrc[q] + at, d.b + (wave * 2 + q) * 1024);
+            for (int q = 0; q < 2; ++q) copy_at(bbase + at, boff[q], d.b + (wave * 2 + q) * 1024);
 #pragma unroll
-        for (int k = 0; k < SG; ++k)
+            for (int k = 0; k < SG; ++k)
 #pragma unroll
-            for (int w = 0; w < 3; ++w) copy_lds4(lesser(ssrc[k] + s * 8 + 4 * w, slast[k]), &d.sc[w][sgroup[k]]);
+                for (int w = 0; w < 3; ++w) copy_lds4(ssrc[k] + s * 8 + 4 * w, &d.sc[w][sgroup[k]]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < RA; ++q) copy_at(abase + at, held(aoff[q], aend - (abase + at)), d.a + (wave * RA + q) * 1024);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) copy_at(bbase + at, held(boff[q], bend - (bbase + at)), d.b + (wave * 2 + q) * 1024);
+#pragma unroll
+            for (int k = 0; k < SG; ++k)
+#pragma unroll
+                for (int w = 0; w < 3; ++w)
+                    copy_lds4(lesser(ssrc[k] + s * 8 + 4 * w, slast[k]), &d.sc[w][sgroup[k]]);
+        }
     };
 
     // the lane's fragment rows and the byte shift of their scales
@@ -365,13 +387,14 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
     const int64_t nkb = mm.K / 32, nslab = (mm.K + 127) / 128;
     const int tail = (int)(mm.K % 128);
 
-    const uint8_t *asrc[Q], *bsrc[Q];
+    uint32_t aoff[Q], boff[Q];                         // as in the forward kernel
+    const uint8_t *const abase = mm.a_codes + m0 * mm.K, *const bbase = mm.b_codes + n0 * mm.K;
     const uint8_t *const aend = mm.a_codes + mm.M * mm.K - 16, *const bend = mm.b_codes + mm.N * mm.K - 16;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int row = (wave * Q + q) * 8 + (lane >> 3), c = swz8(row, lane & 7);
-        asrc[q] = mm.a_codes + min(m0 + row, mm.M - 1) * mm.K + 16 * c;
-        bsrc[q] = mm.b_codes + min(n0 + bwd_column<T>(row), mm.N - 1) * mm.K + 16 * c;
+        aoff[q] = (uint32_t)(min((int64_t)row, mm.M - 1 - m0) * mm.K) + 16 * c;
+        boff[q] = (uint32_t)(min((int64_t)bwd_column<T>(row), mm.N - 1 - n0) * mm.K) + 16 * c;
     }
     auto scale_row = [&](int r) -> const uint8_t * {
         return r < T ? mm.a_scales + min(m0 + r, mm.M - 1) * nkb
@@ -384,14 +407,23 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
     auto issue = [&](int64_t s, int stage) {
         BwdStage<T> &d = st[stage];
         const int64_t at = s * 128;
-        const bool partial = tail && s == nslab - 1;
+        if (s != nslab - 1) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            copy_lds16(partial ? lesser(asrc[q] + at, aend) : asrc[q] + at, d.a + (wave * Q + q) * 1024);
-            copy_lds16(partial ? lesser(bsrc[q] + at, bend) : bsrc[q] + at, d.b + (wave * Q + q) * 1024);
+            for (int q = 0; q < Q; ++q) {
+                copy_at(abase + at, aoff[q], d.a + (wave * Q + q) * 1024);
+                copy_at(bbase + at, boff[q], d.b + (wave * Q + q) * 1024);
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) copy_lds4(ssrc + s * 4 + 4 * w, &d.sc[w][sgroup]);
+        } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                copy_at(abase + at, held(aoff[q], aend - (abase + at)), d.a + (wave * Q + q) * 1024);
+                copy_at(bbase + at, held(boff[q], bend - (bbase + at)), d.b + (wave * Q + q) * 1024);
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) copy_lds4(lesser(ssrc + s * 4 + 4 * w, slast), &d.sc[w][sgroup]);
         }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) copy_lds4(lesser(ssrc + s * 4 + 4 * w, slast), &d.sc[w][sgroup]);
     };
 
     const int kg = lane >> 4, rl = lane & 15;

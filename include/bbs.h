@@ -346,7 +346,7 @@ int grouped_nvfp4_gemm_s2f6(const bbs_fp4 *A, const int32_t *row_index,
  * aligned scales is the fast case of large problems.  A may have a decode
  * scale per row.
  * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale
- * or with different tile2d. */
+ * or with different tile2d, or for K >= 2^25. */
 int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act,
                      void *H, int32_t h_dtype, int64_t ldh, const bbs_mx8 *g8,
                      const bbs_mx8 *u8, void *stream);
@@ -362,7 +362,8 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
  * 16 == 0; they may be the two halves of one M x 2F matrix (ld = 2F), the
  * row operand of the weights' gradient and of the block's input gradient.
  * act as for the forward pass.  K % 128 == 0 with 4-byte aligned scales is
- * the fast case of large problems.  Errors: BBS_EINVAL. */
+ * the fast case of large problems.  Errors: BBS_EINVAL; BBS_ENOTSUP for K >=
+ * 2^25. */
 int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8,
                          const bbs_mx8 *u8, int32_t act, void *dG, void *dU, int32_t dtype,
                          int64_t ld, void *stream);

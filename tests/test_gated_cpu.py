@@ -74,6 +74,14 @@ def bwd(dY=None, Wt=None, g8=None, u8=None, act=0, dG=0x4000, dU=0x5000, dt=1, l
                                   None)
 
 
+def test_k_of_2_to_the_25():
+    """Row offsets inside a tile are 32 bits wide."""
+    K = 1 << 25
+    W = fp4(48, K)
+    assert gated(A=fp4(32, K), Wg=W, Wu=fp4(48, K)) == bbs.BBS_ENOTSUP
+    assert bwd(dY=mx8(24, K), Wt=mx8(96, K)) == bbs.BBS_ENOTSUP
+
+
 def test_gated_bwd_errors():
     assert L.mxfp8_gemm_gated_bwd(None, None, None, None, 0, P(0x4000), P(0x5000), 1, 96, None) == bbs.BBS_EINVAL
     assert bwd(dY=mx8(0, 64)) == bbs.BBS_EINVAL

@@ -698,6 +698,44 @@ def test_nan_rows_do_not_leak(bbs):
         assert torch.equal(bad, want), (M, F, K)
 
 
+def test_longest_k(bbs):
+    """The longest rows: every product of one block near the end, one in the middle."""
+    announce("gated operators: longest K")
+    K, M, F = (1 << 25) - 32, 48, 64
+    A, Wg, Wu = (bbs.NVFP4Tensor.empty(r, K, device=dev()) for r in (M, F, F))
+    dY, Wt = (bbs.MXFP8Tensor.empty(r, K, device=dev()) for r in (M, F))
+    places = torch.tensor([16 * 7, K // 2, K - 48, K - 16], device=dev())
+    small = []
+    for seed, t in enumerate((A, Wg, Wu)):
+        s = random_nv(bbs, t.rows, 64, False, seed)
+        t.codes.zero_(), t.scales.fill_(0x38), t.s_dec.fill_(0.25)
+        for i, at in enumerate(places.tolist()):
+            t.codes[:, at // 2:at // 2 + 8] = s.codes[:, 8 * i:8 * i + 8]
+            t.scales[:, at // 16] = s.scales[:, i]
+        small.append(nv64(s) * 0.25 / s.s_dec.double())
+    mx = []
+    for seed, t in enumerate((dY, Wt)):
+        s = random_mx(bbs, t.rows, 128, seed)
+        t.codes.zero_(), t.scales.zero_()
+        for i, at in enumerate((0, K // 64 * 32, K - 64, K - 32)):
+            t.codes[:, at:at + 32] = s.codes[:, 32 * i:32 * i + 32]
+            t.scales[:, at // 32] = s.scales[:, i]
+        mx.append(mx64(s))
+    h = torch.empty((M, F), dtype=torch.float32, device=dev())
+    bbs.nvfp4_gated_gemm(A, Wg, Wu, h, 0)
+    g8, u8 = random_mx(bbs, M, F, 8, 122), random_mx(bbs, M, F, 9, 121)
+    d = torch.empty((M, 2 * F), dtype=torch.float32, device=dev())
+    bbs.mxfp8_gemm_gated_bwd(dY, Wt, g8, u8, d[:, :F], d[:, F:], 0)
+    (g, Eg), (u, Eu) = product_t(small[0], small[1]), product_t(small[0], small[2])
+    v, _, ea, _ = act_t("silu", g)
+    within(h, v * u, (u.abs() + Eu) * (1.13 * Eg + ea) + v.abs() * Eu + 2 * ULP * (v * u).abs(), False, "h")
+    dh, Ed = product_t(*mx)
+    ga, gb = (t.abs().reshape(len(t), 16, 8).amax(2) for t in mx)      # the matrix instruction's grid
+    Ed = Ed + 7 * 2.0 ** -13 * (ga @ gb.t())
+    a, _, ea, _ = act_t("silu", mx64(g8))
+    within(d[:, F:], dh * a, a.abs() * Ed + (dh.abs() + Ed) * ea + 3 * ULP * (dh * a).abs(), False, "dU")
+
+
 def test_gated_gemm_output_beyond_32_bits(bbs):
     """An output of more than 2^32 bytes and 2^31 elements: the last rows."""
     announce("gated gemm past 2^31 outputs")
