@@ -388,7 +388,7 @@ __global__ __launch_bounds__(64 * kTileSplit) void gemv_tile_kernel(GemvParams p
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * (16 * NR);
-    const int t0 = blockIdx.y * (16 * NT);                // the workgroup's first token
+    const int t0 = NR == 4 ? 0 : blockIdx.y * (16 * NT);  // the workgroup's first token (tile_shape)
     TilePlace<NR> pl;
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
