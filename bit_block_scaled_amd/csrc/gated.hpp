@@ -84,20 +84,24 @@ __device__ __forceinline__ float gate_act(float g) {
     return g * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
-// act(g) and its derivative s + g s (1 - s) dz/dg, with 1 - s taken as
-// e^-z s, which does not cancel for large z (the minimum keeps e^-z finite, so
-// that it is not infinity times 0).
+// act(g) and its derivative s + g s (1 - s) dz/dg for every finite g, with 1 - s
+// taken as e^-z s, which does not cancel for large z.  Where e^-z overflows
+// (z < -88.7) s is 0, and so are both results; the minimum keeps s e^-z from
+// being 0 times infinity there.  GELU's dz/dg grows as g^2 beside a factor
+// that is 0 from |g| = 12 on, and is held to |g| <= 16, so that it stays finite.
 template <int ACT, bool TO_BF16>
 __device__ __forceinline__ float gate_act_grad(float g, float &slope) {
     const float z = gate_z<ACT>(g);
-    const float e = TO_BF16 ? __builtin_amdgcn_exp2f(fminf(z * -1.44269502f, 126.0f))
-                            : fminf(exp_neg(z), 3.0e38f);
+    const float e = TO_BF16 ? __builtin_amdgcn_exp2f(z * -1.44269502f) : exp_neg(z);
     const float s = __builtin_amdgcn_rcpf(1.0f + e);
     const float a = g * s;
-    const float r = a * (s * e);
-    slope = ACT == kActSilu
-                ? s + r
-                : __builtin_fmaf(r, 1.5957691216f * __builtin_fmaf(0.134145f * g, g, 1.0f), s);
+    const float r = a * (s * fminf(e, 3.0e38f));
+    if (ACT == kActSilu) {
+        slope = s + r;
+    } else {
+        const float h = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f);
+        slope = __builtin_fmaf(r, 1.5957691216f * __builtin_fmaf(0.134145f * h, h, 1.0f), s);
+    }
     return a;
 }
 
