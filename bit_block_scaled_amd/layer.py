@@ -47,7 +47,7 @@ from torch.autograd.function import once_differentiable
 
 from . import (ACT_GELU, ACT_SILU, FMT_MXFP8, FMT_NVFP4, GEMV_MAX_TOKENS, OUT_BF16, OUT_F32, SR,
                MXFP8Tensor, NVFP4Tensor, amax_workspace, mxfp8_gemm_gated_bwd, mxfp8_requantize_t,
-               nvfp4_gated_gemm, nvfp4_gated_gemv, nvfp4_gemm, nvfp4_gemv, nvfp4_quantize)
+               nvfp4_gated_gemm, nvfp4_gated_gemv, nvfp4_gemm, nvfp4_gemv, nvfp4_quantize, _on_current)
 
 
 def _bits(t):
@@ -262,6 +262,7 @@ class QGatedMLP(torch.nn.Module):
     def forward(self, x):
         if x.shape[-1] != self.features:
             raise ValueError("last dimension of x must be features")
+        _on_current(None, x, self.w_gate_up, self.w_down)
         tokens = x.numel() // self.features
         if tokens == 0 or tokens % 32:
             raise ValueError("the number of tokens must be a positive multiple of 32")
@@ -287,6 +288,7 @@ class QGatedMLPInference:
         F, K = w_down.shape[1], w_gate_up.shape[1]
         if w_gate_up.shape[0] != 2 * F or any(n == 0 or n % 16 for n in (F, K, w_down.shape[0])):
             raise ValueError("w_gate_up must be [2F, K], w_down [N, F], all multiples of 16")
+        _on_current(None, w_gate_up, w_down)
         self.act = _ACTS[act]
         ws = amax_workspace(w_down.device)
         self._stacked = _nvfp4_weight(w_gate_up, ws)
@@ -297,6 +299,7 @@ class QGatedMLPInference:
         K, F, N = self.gate.cols, self.gate.rows, self.down.rows
         if x.shape[-1] != K:
             raise ValueError("last dimension of x does not fit the weights")
+        _on_current(None, x, self.down.codes)
         lead = x.shape[:-1]
         x2 = x.reshape(-1, K).to(torch.bfloat16).contiguous()
         T, dev = x2.shape[0], x.device

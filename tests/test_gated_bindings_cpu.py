@@ -1,4 +1,4 @@
-"""The Python calls of the gated and the few-token operators
+"""The Python calls of the gated and the few-token operators, and their layers,
 refuse tensors that the C ABI would take for something else: host memory,
 another type, shapes too small, elements of a row that are not adjacent,
 weights of another format.  Nothing is launched."""
@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import bit_block_scaled_amd as bbs                                          # noqa: E402
+from bit_block_scaled_amd import layer                                      # noqa: E402
 
 M, F, K = 32, 64, 96
 
@@ -85,6 +86,13 @@ def test_gated_bwd():
     call("dU must", dU=bf(M, 2 * F)[:, ::2])
     call("row stride", dU=bf(M, 2 * F)[:, :F])
     call("dU must", dG=bf(M, F + 8), ld=F + 8)
+
+
+def test_layers():
+    b = layer.QGatedMLP(64, 96, device="cpu")
+    refused("GPU", b, bf(32, 64))
+    refused("GPU", b.inference)
+    refused("GPU", layer.QGatedMLPInference, b.w_gate_up.detach(), b.w_down.detach())
 
 
 def test_packed_descriptors():
