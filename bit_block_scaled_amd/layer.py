@@ -37,7 +37,8 @@ backward  dY -> the NVFP4 copy of dY^T and MXFP8 rows; Wd's copy -> MXFP8 of
           (MXFP8).
 
 Kept for the backward pass, in bits a value: 4.5 for X, 4.5 + 2 * 8.25 for the
-hidden values.  Call t draws from Philox streams 8t .. 8t + 7.
+hidden values, and of those only what the wanted gradients read (nothing under
+torch.no_grad).  Call t draws from Philox streams 8t .. 8t + 7.
 QGatedMLPInference holds the quantized weights of such a block and answers
 with the matrix-vector kernels (activations in BF16) up to GEMV_MAX_TOKENS
 tokens, with the GEMMs beyond.
@@ -165,33 +166,35 @@ class QGatedMLPFn(torch.autograd.Function):
     w_down [N, F]."""
 
     @staticmethod
-    def forward(ctx, x, w_gate_up, w_down, act, seed, step, signs):
+    def forward(ctx, x, w_gate_up, w_down, act, seed, step, signs, grad=True):
+        """grad: whether the call is recorded (a Function does not see grad mode itself)."""
         lead, K = x.shape[:-1], x.shape[-1]
         F, N = w_gate_up.shape[0] // 2, w_down.shape[0]
         x2 = _bits(x.reshape(-1, K))
         M, dev = x2.shape[0], x.device
         ws = amax_workspace(dev)
-        train = any(ctx.needs_input_grad)
+        need_x, need_gu, need_d = (grad and n for n in ctx.needs_input_grad[:3])
+        need_h = need_x or need_gu           # the backward pass reaches the activation
 
-        def copies(t, rows, cols, stream):
+        def copies(t, rows, cols, stream, keep):
             q = NVFP4Tensor.empty(rows, cols, device=dev)
-            c = NVFP4Tensor.empty(cols, rows, device=dev) if train else None
-            nvfp4_quantize(t, q, c, col_round=SR, col_rng=(seed, stream), col_rht=train, rht_signs=signs,
+            c = NVFP4Tensor.empty(cols, rows, device=dev) if keep else None
+            nvfp4_quantize(t, q, c, col_round=SR, col_rng=(seed, stream), col_rht=keep, rht_signs=signs,
                            amax_ws=ws)
             return q, c
 
-        xq, xc = copies(x2, M, K, 8 * step)
+        xq, xc = copies(x2, M, K, 8 * step, need_gu)
         wq = _nvfp4_weight(w_gate_up, ws)
         h = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
-        g8, u8 = (MXFP8Tensor.empty(M, F, device=dev) if train else None for _ in range(2))
+        g8, u8 = (MXFP8Tensor.empty(M, F, device=dev) if need_h else None for _ in range(2))
         nvfp4_gated_gemm(xq, *_halves(wq), h, OUT_BF16, act=act, g_ckpt=g8, u_ckpt=u8)
-        hq, hc = copies(h.view(torch.int16), M, F, 8 * step + 1)
+        hq, hc = copies(h.view(torch.int16), M, F, 8 * step + 1, need_d)
         dq = _nvfp4_weight(w_down, ws)
         y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
         nvfp4_gemm(FMT_NVFP4, hq, dq, y, OUT_BF16)
-        if train:
-            ctx.save_for_backward(*(t for q in (xc, wq, hc, dq) for t in (q.codes, q.scales, q.s_dec)),
-                                  g8.codes, g8.scales, u8.codes, u8.scales)
+        kept4 = (xc, wq if need_x else None, hc, dq if need_h else None)
+        ctx.save_for_backward(*(t for q in kept4 for t in ((q.codes, q.scales, q.s_dec) if q else (None,) * 3)),
+                              *(t for q in (g8, u8) for t in ((q.codes, q.scales) if q else (None,) * 2)))
         ctx.dims = (M, K, F, N, lead, w_gate_up.dtype, w_down.dtype)
         ctx.args = (act, seed, step, signs)
         return y.reshape(*lead, N)
@@ -235,7 +238,7 @@ class QGatedMLPFn(torch.autograd.Function):
                 dx = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
                 nvfp4_gemm(FMT_MXFP8, gm, wt, dx, OUT_BF16)
                 dx = dx.reshape(*lead, K)
-        return dx, dw_gate_up, dw_down, None, None, None, None
+        return dx, dw_gate_up, dw_down, None, None, None, None, None
 
 
 class QGatedMLP(torch.nn.Module):
@@ -267,7 +270,7 @@ class QGatedMLP(torch.nn.Module):
         if tokens == 0 or tokens % 32:
             raise ValueError("the number of tokens must be a positive multiple of 32")
         y = QGatedMLPFn.apply(x, self.w_gate_up, self.w_down, _ACTS[self.act], self.seed, self.step,
-                              self.rht_signs)
+                              self.rht_signs, torch.is_grad_enabled())
         self.step += 1
         return y
 
