@@ -18,7 +18,7 @@ __device__ __forceinline__ void run_out(big::Smem &sm, float *tab, const GemmPar
                                      [&](int64_t m) { return scale_of(m, g); }, p.c, p.ldc, wm, wn, lane, p.q);
     };
     big::run_tiles<BT, NJ>(sm, tab, OUT == big::OUT_QG ? p.q.gelu_tab : nullptr, p.a, p.K, p.N, next_tile,
-                           [&](int g) { return big::PlainB{b_view(g)}; }, a_row, finish);
+                           b_view, a_row, finish);
 }
 
 template <int OUT>
