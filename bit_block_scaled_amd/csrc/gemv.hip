@@ -607,9 +607,25 @@ hipError_t by_act(const GemvParams &p, hipStream_t s) {
 
 }  // namespace
 
+// A launch has fewer than 2^32 threads a dimension (more are cut off without an
+// error), and the kernels take up to 64 a row: more than 2^25 rows go in parts.
 hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s) {
-    if (mxfp4) return by_act<kRows32>(p, s);
-    return p.tile2d ? by_act<kTiles16>(p, s) : by_act<kRows16>(p, s);
+    constexpr int64_t kRows = (int64_t)1 << 25;
+    GemvParams q = p;
+    for (int64_t n = 0; n < p.N; n += kRows) {
+        q.N = std::min(kRows, p.N - n);
+        q.y = static_cast<uint8_t *>(p.y) + n * (p.bf16_out ? 2 : 4);
+        for (auto w : {&GemvParams::w, &GemvParams::u}) {
+            if (p.act < 0 && w == &GemvParams::u) continue;
+            (q.*w).codes = (p.*w).codes + n * (p.K / 2);
+            (q.*w).scales = (p.*w).scales + (mxfp4 ? n * (p.K / 32) : (p.tile2d ? n / 16 : n) * (p.K / 16));
+        }
+        const hipError_t e = mxfp4      ? by_act<kRows32>(q, s)
+                             : p.tile2d ? by_act<kTiles16>(q, s)
+                                        : by_act<kRows16>(q, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace bbs

@@ -105,3 +105,26 @@ def test_slope_over_every_checkpoint_value(bbs, M, F, K, bf16, act):
     ea, es = bounds(act, g)
     check(got[0], sl, es, bf16, g, "slope")
     check(got[1], a, ea, bf16, g, "act")
+
+
+@pytest.mark.parametrize("T,N,gated", [(1, (1 << 30) + 4096, False), (2, (1 << 29) + 4112, True)])
+def test_rows_beyond_a_launch(bbs, T, N, gated):
+    """More rows than one launch has threads for: every output is written.  K = 16, weights 1
+    and 2 by parts of 2^20 rows, so y = 16 or 32 times the token's value."""
+    announce(f"gemv {T} x {N} rows, gated={gated}")
+    K = 16
+    part = (torch.arange(N, device=dev()) >> 20) % 2
+    codes = torch.where(part.bool(), 0x44, 0x22).to(torch.uint8)[:, None].repeat(1, K // 2)
+    W = bbs.NVFP4Tensor(codes, torch.full((N, 1), 0x38, dtype=torch.uint8, device=dev()),
+                        torch.ones(1, device=dev()), N, K, False)
+    x = torch.arange(1, T + 1, device=dev()).bfloat16()[:, None].repeat(1, K)
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device=dev())
+    if gated:
+        bbs.nvfp4_gated_gemv(0, x, W, W, y, 1)
+    else:
+        bbs.nvfp4_gemv(0, x, W, y, 1)
+    for t in range(T):
+        ref = 16.0 * (t + 1) * (1 + part.float())
+        if gated:
+            ref = ref * ref                        # SiLU of 16 and more is g (1 - 2^-23 at most)
+        assert torch.equal(y[t].float(), ref.bfloat16().float()), t
