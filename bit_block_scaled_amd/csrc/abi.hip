@@ -683,6 +683,15 @@ int check_rows_out(const void *p, int32_t dtype, int64_t cols, int64_t ld, const
     return BBS_OK;
 }
 
+// A launch of 2^32 threads or more is cut off without an error, and the
+// small-tile kernels have 256 threads a tile (TM x TN where there are many).
+int check_tiles(int64_t M, int64_t N, int64_t TM, int64_t TN) {
+    const int64_t tm = (M + TM - 1) / TM, tn = (N + TN - 1) / TN;
+    if (tm > (((int64_t)1 << 24) - 1) / tn)
+        return fail(BBS_ENOTSUP, "an output of 2^24 tiles of %lld x %lld or more", (long long)TM, (long long)TN);
+    return BBS_OK;
+}
+
 // Shared checks of nvfp4_gemv (Wu null) and nvfp4_gated_gemv.
 int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
               const void *Wu, bool gated, int32_t act, void *y, int32_t y_dtype, int64_t ldy,
@@ -771,6 +780,7 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
     if (Wg->tile2d != Wu->tile2d) return fail(BBS_ENOTSUP, "Wg and Wu with different tile2d");
     // row offsets inside a tile are 32 bits wide
     if (A->cols >= (int64_t)1 << 25) return fail(BBS_ENOTSUP, "2^25 columns or more");
+    if ((st = check_tiles(A->rows, Wg->rows, 256, 64))) return st;
     if ((st = check_rows_out(H, h_dtype, Wg->rows, ldh, "H"))) return st;
     if (!g8 != !u8) return fail(BBS_EINVAL, "g8 and u8 come together");
     bbs::GatedParams p{};
@@ -809,6 +819,7 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
     if (!act_ok(act)) return fail(BBS_EINVAL, "bad act");
     if (dY->cols != Wt->cols) return fail(BBS_EINVAL, "dY.cols != Wt.cols");
     if (dY->cols >= (int64_t)1 << 25) return fail(BBS_ENOTSUP, "2^25 columns or more");   // as above
+    if ((st = check_tiles(dY->rows, Wt->rows, 128, 128))) return st;
     for (const bbs_mx8 *c : {g8, u8})
         if (c->rows != dY->rows || c->cols != Wt->rows)
             return fail(BBS_EINVAL, "g8 and u8 must be dY.rows x Wt.rows");

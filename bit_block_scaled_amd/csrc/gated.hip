@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t held(uint32_t off, int64_t last) { return (u
 // Tile of workgroup b: workgroup b runs on XCD b % 8, so each XCD is given a
 // contiguous range of tile ids, and ids walk 8 row tiles down before moving
 // along the columns, which keeps operand panels in one XCD's L2.  In 32 bits
-// (the launch holds the tiles to 2^31 - 1), as 64-bit divisions are long
+// (the launch holds the tiles below 2^24), as 64-bit divisions are long
 // (64 x 512 x 512: 8.3 us against 8.6).
 __device__ __forceinline__ void tile_of(uint32_t tm, uint32_t tn, int64_t &mt, int64_t &nt) {
     const uint32_t total = tm * tn, x = blockIdx.x % 8, share = total / 8, extra = total % 8;
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
 // Launch with dynamic LDS; the kernel's limit is raised once per kernel.
 template <auto Kernel, typename Params>
 hipError_t launch(int64_t tiles, int threads, size_t shm, const Params &p, hipStream_t s) {
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    if (tiles * threads > UINT32_MAX) return hipErrorInvalidConfiguration;    // would be cut off
     static const bool attr_set = [shm] {
         (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
                                   hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);

@@ -346,7 +346,8 @@ int grouped_nvfp4_gemm_s2f6(const bbs_fp4 *A, const int32_t *row_index,
  * aligned scales is the fast case of large problems.  A may have a decode
  * scale per row.
  * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale
- * or with different tile2d, or for K >= 2^25. */
+ * or with different tile2d, for K >= 2^25, or for an output of 2^24 tiles of
+ * 256 x 64 or more. */
 int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act,
                      void *H, int32_t h_dtype, int64_t ldh, const bbs_mx8 *g8,
                      const bbs_mx8 *u8, void *stream);
@@ -363,7 +364,7 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
  * row operand of the weights' gradient and of the block's input gradient.
  * act as for the forward pass.  K % 128 == 0 with 4-byte aligned scales is
  * the fast case of large problems.  Errors: BBS_EINVAL; BBS_ENOTSUP for K >=
- * 2^25. */
+ * 2^25 or an output of 2^24 tiles of 128 x 128 or more. */
 int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8,
                          const bbs_mx8 *u8, int32_t act, void *dG, void *dU, int32_t dtype,
                          int64_t ld, void *stream);
