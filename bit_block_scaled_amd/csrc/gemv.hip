@@ -535,9 +535,14 @@ hipError_t tile(const GemvParams &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Rows of a workgroup, over both matrices of the gated form: 16 where that
-// still gives every CU one (one token, 4096 x 14336: 8.1 us with 16 rows, 8.4
-// with 8), 8 below (1536 x 4096: 3.2 us with 8 rows, 3.7 with 16, 3.4 with 4).
+// Rows of a workgroup, over both matrices of the gated form: 16 from 4096 rows
+// of a matrix on, which is one workgroup for each of 256 CUs and two in the
+// gated form, and 8 below.
+//   1 token, 4096 x 14336: 8.1 us with 16 rows, 8.4 with 8
+//   1 token, 1536 x 4096: 3.2 us with 8 rows, 3.7 with 16, 3.4 with 4
+// Gated, between one and two workgroups of 16 a CU, the number of rows and K
+// decide: 2064 x 1024 3.2 us with 8 rows, 3.5 with 16; 3008 x 4096 5.2 and 5.8;
+// 2048 x 4096 4.4 and 4.4; 4080 x 8192 10.0 and 8.6.
 template <int SC, int NM, int TT>
 hipError_t few_rows(const GemvParams &p, hipStream_t s) {
     return p.N >= 4096 ? few<SC, NM, TT, 4 / NM>(p, s) : few<SC, NM, TT, 2 / NM>(p, s);

@@ -283,7 +283,10 @@ class QGatedMLPInference:
     """y = (act(x Wg^T) * (x Wu^T)) Wd^T from NVFP4 weights that are quantized
     when the object is made (later changes of the given weights do not reach
     it).  Up to GEMV_MAX_TOKENS tokens the activations stay BF16; more tokens
-    are quantized to NVFP4 (padded to a multiple of 16 rows) for the GEMMs."""
+    are quantized to NVFP4 (padded to a multiple of 16 rows) for the GEMMs, with
+    one decode scale for the call, so a token's answer then also depends on the
+    other tokens.  Callers that need BF16 activations give GEMV_MAX_TOKENS
+    tokens at a time."""
 
     def __init__(self, w_gate_up, w_down, act="silu"):
         if act not in _ACTS:

@@ -356,7 +356,8 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
  * checkpoints, in one kernel: with dH = dY * Wt^T (as the MXFP8 nvfp4_gemm,
  * in FP32, never stored) and g, u decoded from g8, u8,
  *   dG = dH * u * act'(g),   dU = dH * act(g),
- * computed in FP32 and rounded once to dtype.  dY is M x K (the gradient of
+ * computed in FP32, from left to right (dH and dH * u must be finite; g may be
+ * any finite value), and rounded once to dtype.  dY is M x K (the gradient of
  * the block's output), Wt is F x K (the down projection's weight transposed,
  * e.g. by mxfp8_requantize_t), g8 and u8 are M x F.  dG and dU are M x F
  * with the same row stride ld (>= F) elements, 16-byte aligned, ld * size %
@@ -376,8 +377,11 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
  *      decode scale), fmt == BBS_FMT_MXFP4: a const bbs_mx4 *.
  * x is tokens x K (BF16 patterns, row stride ldx elements, ldx % 8 == 0,
  * 16-byte aligned), W is N x K, y is tokens x N with row stride ldy (>= N)
- * elements.  A weight (code times scale) must be below 2^128.  The order of the sums
- * depends on the sizes alone, so the same call gives the same bits.
+ * elements.  A weight (code times scale) must be below 2^128, and so must the
+ * sum of 16 activations times their codes (|x| < 2^121 is enough), besides the
+ * sums themselves.  The order of the sums depends on the sizes, the format and
+ * the device's number of CUs, so the same call on the same device gives the
+ * same bits.
  * Errors: BBS_EINVAL; BBS_ENOTSUP for a weight with a per-row decode scale,
  * or with more than 2^31 - 1 rows or 2^26 columns. */
 int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,

@@ -128,3 +128,32 @@ def test_rows_beyond_a_launch(bbs, T, N, gated):
         if gated:
             ref = ref * ref                        # SiLU of 16 and more is g (1 - 2^-23 at most)
         assert torch.equal(y[t].float(), ref.bfloat16().float()), t
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 64])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_longest_rows_of_the_few_token_products(bbs, T, fmt):
+    """K = 2^26, the most the calls take, and 80 rows: a weight of 2 in the last place of row n,
+    one of 1 at n 2^19 and zeros elsewhere, x counting in powers of two."""
+    announce(f"gemv {T} x 80 x 2^26 {fmt}")
+    N, K = 80, 1 << 26
+    codes = torch.zeros((N, K // 2), dtype=torch.uint8, device=dev())
+    at = torch.arange(N, device=dev()) << 19
+    codes[torch.arange(N, device=dev()), at // 2] = 2                     # 1 in the even column
+    codes[:, -1] = 4 << 4                                                 # 2 in the last column
+    x = torch.zeros((T, K), dtype=torch.bfloat16, device=dev())
+    x[:, at] = torch.exp2((torch.arange(N, device=dev()) % 7).double()).bfloat16()
+    x[:, -1] = torch.arange(1, T + 1, device=dev()).bfloat16()
+    if fmt == "nvfp4":
+        W = bbs.NVFP4Tensor(codes, torch.full((N, K // 16), 0x38, dtype=torch.uint8, device=dev()),
+                            torch.ones(1, device=dev()), N, K, False)
+    else:
+        W = bbs.MXFP4Tensor(codes, torch.full((N, K // 32), 127, dtype=torch.uint8, device=dev()), N, K)
+    y, h = (torch.full((T, N), 7.0, dtype=torch.float32, device=dev()) for _ in range(2))
+    bbs.nvfp4_gemv(0 if fmt == "nvfp4" else 2, x, W, y, 0)
+    bbs.nvfp4_gated_gemv(0 if fmt == "nvfp4" else 2, x, W, W, h, 0)
+    t, n = np.arange(1, T + 1)[:, None], np.arange(N)[None]
+    ref = np.exp2(n % 7) + 2.0 * t
+    assert np.array_equal(host(y).astype(np.float64), ref)
+    sq, E = ref * act64("silu", ref), 32 * ULP * ref * ref                # 16 roundings, and 6 of z
+    assert np.all(np.abs(host(h) - sq) <= E)
