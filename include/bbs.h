@@ -357,7 +357,9 @@ int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int
  * in FP32, never stored) and g, u decoded from g8, u8,
  *   dG = dH * u * act'(g),   dU = dH * act(g),
  * computed in FP32, from left to right (dH and dH * u must be finite; g may be
- * any finite value), and rounded once to dtype.  dY is M x K (the gradient of
+ * any finite value), and rounded once to dtype.  The FP8 product adds each
+ * aligned group of eight products on a grid 2^-13 below the group's largest, so
+ * dH is 2e-5 off (relative norm) whatever dtype is.  dY is M x K (the gradient of
  * the block's output), Wt is F x K (the down projection's weight transposed,
  * e.g. by mxfp8_requantize_t), g8 and u8 are M x F.  dG and dU are M x F
  * with the same row stride ld (>= F) elements, 16-byte aligned, ld * size %
