@@ -46,7 +46,7 @@ ROTATE = 8                                     # buffer sets the timed runs cycl
 # WRITE_SIZE runs scaled by what the same counters read for the 512 MiB copy
 # (profiles/sq_hbm_counters_step_kernels_8192x4096x14336.md), valid only for the kernel
 # sources they were taken on: reported as null once those sources change.
-FPROP_TRAFFIC = {"bytes": 626582912, "sources_sha256_16": "faf04c03a681f2fb"}
+FPROP_TRAFFIC = {"bytes": 626717330, "sources_sha256_16": "2636448cdfe2748c"}
 FPROP_SOURCES = ["bit_block_scaled_amd/csrc/gemm_nvfp4.hip", "bit_block_scaled_amd/csrc/gemm_nvfp4_tiles.hpp",
                  "bit_block_scaled_amd/csrc/bbs_device.hpp", "bit_block_scaled_amd/csrc/bbs_kernels.hpp",
                  "bit_block_scaled_amd/build.py"]

@@ -276,12 +276,12 @@ __global__ __launch_bounds__(64 * kFewSplit) void gemv_few_kernel(GemvParams p) 
 // one fragment read fall on sixteen different bank groups.
 //
 // Bound by the latency of a step and the L1 accesses of scattered rows: MXFP4
-// 14336 x 4096 (32 MB) takes 16.6 us for 48 tokens; without the activations'
-// copies it would be 12.8, without the weights' loads 12.1.  NVFP4 with 16x16
-// scales takes 10.3 us for up to 16 tokens, with 1x16 scales 12.8.  A step
-// ahead in registers, two steps a fetch, twice the waves, activations shared by
-// two row halves and a rotated order of K each changed it by less than 5% or
-// made it slower.
+// 14336 x 4096 (32 MB) takes 15.4 us for 48 tokens in a graph and 16.3 in a
+// kernel trace; where it took 16.6, it took 12.8 without the activations' copies
+// and 12.1 without the weights' loads.  NVFP4 with 16x16 scales takes 10.0 us for
+// up to 16 tokens, with 1x16 scales 12.8.  A step ahead in registers, two steps a
+// fetch, twice the waves, activations shared by two row halves and a rotated
+// order of K each changed it by less than 5% or made it slower.
 // ---------------------------------------------------------------------------
 constexpr int kTileK = 128;
 constexpr int kTileSplit = 8;    // most waves of a workgroup (K splits)
