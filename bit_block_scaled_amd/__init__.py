@@ -1,7 +1,8 @@
 """Python binding of libbbs.so, the MI355X NVFP4 quantized-linear library.
 
-Argument marshalling only: every step of the hot path runs in the HIP kernels
-behind the C ABI declared in include/bbs.h.  PyTorch is used for device
+Argument marshalling, and for the gated and the few-token calls checks of what a
+pointer does not tell: every step of the hot path runs in the HIP kernels behind
+the C ABI declared in include/bbs.h.  PyTorch is used for device
 memory and streams.  The functions have the names of the C entry points and
 raise BbsError on a non-zero status.  There is no CPU fallback: importing
 this module fails if the library has not been built.
