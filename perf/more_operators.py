@@ -32,31 +32,31 @@ def listed():
 
     return [
         # a prompt's up projection at sizes that fill no tile and no slab
-        linear("linear, odd sizes", 528, 2736, 1552, act="gelu", bias="f32", tile=False, out="f32"),
+        linear("linear odd sizes", 528, 2736, 1552, act="gelu", bias="f32", tile=False, out="f32"),
         # a short prompt's down projection back into the residual stream
-        linear("linear, short prompt", 256, 4096, 1536, bias="bf16", residual=True, out="f32"),
+        linear("linear short prompt", 256, 4096, 1536, bias="bf16", residual=True, out="f32"),
         # long prompts through the dense down projection, into the residual stream
-        linear("linear, dense down", 8192, 4096, 14336, bias="bf16", residual=True),
+        linear("linear dense down", 8192, 4096, 14336, bias="bf16", residual=True),
         # a training step at sizes that fill no tile and no slab
-        linear("linear train, odd sizes", 272, 1568, 1184, act="silu", bias="f32", tile=False, op="linear_train"),
+        linear("linear train odd sizes", 272, 1568, 1184, act="silu", bias="f32", tile=False, op="linear_train"),
         # a training step of the dense up projection
-        linear("linear train, dense up", 8192, 14336, 4096, act="gelu", bias="bf16", op="linear_train"),
+        linear("linear train dense up", 8192, 14336, 4096, act="gelu", bias="bf16", op="linear_train"),
         # one token through a small up projection: latency counts
-        linear("linear gemv, 1 token", 1, 1536, 4096, act="gelu", bias="bf16", op="linear_gemv"),
+        linear("linear gemv 1 token", 1, 1536, 4096, act="gelu", bias="bf16", op="linear_gemv"),
         # a batch of sequences, one token each, through the dense down projection
-        linear("linear gemv, 40 tokens", 40, 4096, 14336, bias="f32", residual=True, tile=False, op="linear_gemv",
+        linear("linear gemv 40 tokens", 40, 4096, 14336, bias="f32", residual=True, tile=False, op="linear_gemv",
                fmt="mxfp4", out="f32"),
         # one token through 8 of 64 plain experts
-        moe("moe, 1 token, 8 of 64", 1, 64, 8, 1536, 4096, act="gelu", gated=False),
+        moe("moe 1 token 8 of 64", 1, 64, 8, 1536, 4096, act="gelu", gated=False),
         # one token through 2 of 8 experts as wide as the dense block
-        moe("moe, 1 token, 2 of 8", 1, 8, 2, 14336, 4096, residual=True),
+        moe("moe 1 token 2 of 8", 1, 8, 2, 14336, 4096, residual=True),
         # a few sequences at odd sizes, some slots dropped for lack of room
-        moe("moe, 5 tokens, odd sizes", 5, 12, 3, 736, 1568, act="gelu", fmt="mxfp4", tile=False, residual=True,
+        moe("moe 5 tokens odd sizes", 5, 12, 3, 736, 1568, act="gelu", fmt="mxfp4", tile=False, residual=True,
             dropped=True, out="f32"),
         # a small batch of sequences, MXFP4 experts
-        moe("moe, 16 tokens, mxfp4", 16, 64, 8, 1536, 4096, fmt="mxfp4", tile=False, residual=True),
+        moe("moe 16 tokens mxfp4", 16, 64, 8, 1536, 4096, fmt="mxfp4", tile=False, residual=True),
         # the largest batch: nearly every expert is read
-        moe("moe, 64 tokens, 8 of 64", 64, 64, 8, 1536, 4096, residual=True),
+        moe("moe 64 tokens 8 of 64", 64, 64, 8, 1536, 4096, residual=True),
     ]
 
 
