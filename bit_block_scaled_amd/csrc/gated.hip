@@ -6,20 +6,10 @@
 //   backward  dh = dY W (MXFP8 x MXFP8), dg = dh * u * act'(g),
 //             du = dh * act(g), with g and u read back from the checkpoints
 //
-// A workgroup of four waves (2 x 2) walks K in slabs of 128 through a ring of
-// LDS stages filled by asynchronous copies, as the large-tile kernels do, but
-// with tiles small enough for two or more workgroups a CU: one's arithmetic
-// covers another's waits, and a problem of a few hundred rows still reaches
-// every CU.
-//
-// K's last slab may be partial and rows may start at any multiple of 8 bytes
-// (codes) or at any byte (scales).  Codes are copied in 16-byte pieces from
-// where they are; what a piece reads past K belongs to the next row and is
-// cancelled by a zero scale, or overwritten by zeros where a code could be NaN.
-// Scales are copied as the aligned words that contain them and shifted into
-// place when they are read; the shift is the same in every slab.  No copy
-// leaves the operand's own bytes but for the rest of the words at its ends.
-#include "gemm_nvfp4_tiles.hpp"
+// The forward kernel is the small-tile engine of the NVFP4 products; the backward
+// kernel walks K the same way.  There what a copied piece reads past K is
+// overwritten by zeros where a code could be NaN.
+#include "gemm_nvfp4_small.hpp"
 #include "gated_epilogue.hpp"
 
 namespace bbs {
@@ -29,60 +19,9 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 namespace {
 
-constexpr int kThreads = 256;
-
-// The aligned word at or before p, and the last one an array [p, p + bytes) touches.
-__device__ __forceinline__ const uint8_t *word_of(const uint8_t *p) {
-    return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3);
-}
-__device__ __forceinline__ const uint8_t *lesser(const uint8_t *a, const uint8_t *b) { return a < b ? a : b; }
-
-// copy_lds16 from base + off, base the same for the wave.  A scalar register
-// that a vector instruction wrote may be read by a memory instruction five
-// wait states later, which the compiler does not see to in front of an asm.
-__device__ __forceinline__ void copy_at(const uint8_t *base, uint32_t off, const void *lds) {
-    const uint64_t b = reinterpret_cast<uint64_t>(base);
-    const uint64_t sb = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32)) << 32 |
-                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
-    asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(sb), "{m0}"(lds_addr(lds))
-                 : "memory");
-}
-
-// An offset held to at most `last`, which is not negative.
-__device__ __forceinline__ uint32_t held(uint32_t off, int64_t last) { return (uint32_t)min((int64_t)off, last); }
-
-// Tile of workgroup b: workgroup b runs on XCD b % 8, so each XCD is given a
-// contiguous range of tile ids, and ids walk 8 row tiles down before moving
-// along the columns, which keeps operand panels in one XCD's L2.  In 32 bits
-// (the launch holds the tiles below 2^24), as 64-bit divisions are long
-// (64 x 512 x 512: 8.3 us against 8.6).
-__device__ __forceinline__ void tile_of(uint32_t tm, uint32_t tn, int64_t &mt, int64_t &nt) {
-    const uint32_t total = tm * tn, x = blockIdx.x % 8, share = total / 8, extra = total % 8;
-    const uint32_t id = x * share + (x < extra ? x : extra) + blockIdx.x / 8;
-    const uint32_t g = id / (8 * tn), in = id - g * (8 * tn);
-    const uint32_t gm = tm - g * 8 < 8 ? tm - g * 8 : 8;
-    mt = g * 8 + in % gm;
-    nt = in / gm;
-}
-
-// Adds the sums of groups 1 .. G - 1 to group 0's, in that order.
-template <int G, int NV>
-__device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, int lane, float (&v)[NV]) {
-    if (G == 1) return;
-    __syncthreads();                               // the rings are free
-    float *const part = reinterpret_cast<float *>(smem) + (wave * NV) * 64 + lane;
-    if (grp) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) part[((grp - 1) * 4 * NV + i) * 64] = v[i];
-    }
-    __syncthreads();
-    if (!grp) {
-#pragma unroll
-        for (int g = 1; g < G; ++g)
-#pragma unroll
-            for (int i = 0; i < NV; ++i) v[i] += part[((g - 1) * 4 * NV + i) * 64];
-    }
-}
+using small::kThreads;
+using small::copy_at, small::held, small::join_groups, small::lesser, small::launch, small::run_tile;
+using small::GatedSide, small::tile_of, small::tiles_of, small::word_of;
 
 // ---------------------------------------------------------------------------
 // Forward: TM rows by 64 columns of both products.
@@ -95,247 +34,46 @@ __device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, in
 // Reading the next slab's codes into registers a step ahead, with a ring one
 // stage deeper, made it slower by 5%, so it is not the copies' latency.
 // ---------------------------------------------------------------------------
-constexpr int kBF = 64;
-
-template <int TM>
-struct FwdStage {
-    uint8_t a[TM * 64];              // 64 code bytes a row and slab, swizzled as big::Stage
-    uint8_t b[2 * kBF * 64];
-    uint32_t sc[3][TM + 2 * kBF];    // the words that hold a row's 8 scale bytes (A rows, then B rows)
-};
-
-// The tile's B rows alternate 32 rows of the gate matrix and the same 32 of the
-// up matrix.  The product's blocks give lane half h rows 8 q + 4 h + e of each
-// 32, which hold columns 16 h + 4 q + e of the block: a lane's outputs are then
-// 16 consecutive columns, and its half of a checkpoint's block one store.
-__device__ __forceinline__ int b_column(int r) {
-    return 32 * (r >> 6) + 16 * (r >> 2 & 1) + 4 * (r >> 3 & 3) + (r & 3);
-}
-// Row of the gate matrix' column c (the up matrix' row is 32 further).
-__device__ __forceinline__ int b_row(int c) {
-    return 64 * (c >> 5) + 8 * (c >> 2 & 3) + 4 * (c >> 4 & 1) + (c & 3);
-}
-
 template <int TM, int NS, int G, int ACT, bool BF16_OUT>
 __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void gated_gemm_kernel(GatedParams p) {
     constexpr int RA = TM / 64;                    // 32-row blocks of a wave
-    constexpr int SG = TM > 128 ? 2 : 1;           // groups of 64 scale rows a wave copies
-    constexpr int kIssued = RA + 2 + 3 * SG;       // copies one wave issues a slab
-    constexpr int AHEAD = NS - 1;                  // slabs in flight beyond the one consumed
     extern __shared__ __align__(16) uint8_t smem[];
-    // four waves a group; group g of G takes slabs g, g + G, ... in its own ring
-    const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-    FwdStage<TM> *const st = reinterpret_cast<FwdStage<TM> *>(smem) + grp * NS;
-    const int t = threadIdx.x & 255, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int wm = wave >> 1, wn = wave & 1;
-    int64_t m0, n0;
-    tile_of((uint32_t)((p.M + TM - 1) / TM), (uint32_t)((p.N + kBF - 1) / kBF), m0, n0);
-    m0 *= TM;
-    n0 *= kBF;
-    const int64_t kb = p.K / 2, ks = p.K / 16;
-    const int64_t nslab = (p.K + 127) / 128;
-    const int tail = (int)(p.K % 128);             // K values of a partial last slab, 0: none
-
-    // copy sources (rows past the end are clamped: they feed nothing that is written)
-    // as 32-bit offsets (K < 2^25) from the tile's first row, which need no
-    // address arithmetic a copy; a wave copies rows of one weight matrix
-    uint32_t aoff[RA], boff[2];
-    const uint8_t *const abase = p.a.codes + m0 * kb, *const aend = p.a.codes + p.a.rows * kb - 16;
-    const uint8_t *const wcodes = (wave & 1 ? p.u : p.b).codes;
-    const uint8_t *const bbase = wcodes + n0 * kb, *const bend = wcodes + p.N * kb - 16;
-    const int pos = big::swz(lane >> 2, lane & 3);
+    auto finish = [](const GatedParams &p, const f32x16 (&acc)[RA][2], int64_t mw, int64_t n0, int wn, int lane)
+                      __attribute__((always_inline)) {
+        const int h = lane >> 5, rl = lane & 31;
+        const float sg = p.b.s_dec[0], su = p.u.s_dec[0];
+        const int64_t n = n0 + wn * 32 + 16 * h;               // the lane's first column
 #pragma unroll
-    for (int q = 0; q < RA; ++q)
-        aoff[q] = (uint32_t)(min((int64_t)((wave * RA + q) * 16 + (lane >> 2)), p.M - 1 - m0) * kb) + 16 * pos;
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        boff[q] = (uint32_t)(min((int64_t)b_column((wave * 2 + q) * 16 + (lane >> 2)), p.N - 1 - n0) * kb) + 16 * pos;
-    // scales: the words of a row's bytes, 64 rows a copy (the waves past the
-    // last row repeat the last 64)
-    auto scale_row = [&](int r) -> const uint8_t * {
-        if (r < TM) {
-            const int64_t m = min(m0 + r, p.M - 1);
-            return p.a.scales + (p.a.tile2d ? m / 16 : m) * ks;
-        }
-        const Fp4View &W = (((r - TM) >> 5) & 1) ? p.u : p.b;
-        const int64_t n = min(n0 + b_column(r - TM), p.N - 1);
-        return W.scales + (W.tile2d ? n / 16 : n) * ks;
-    };
-    int sgroup[SG];
-    const uint8_t *ssrc[SG], *slast[SG];
-#pragma unroll
-    for (int k = 0; k < SG; ++k) {
-        sgroup[k] = min(wave * SG + k, (TM + 2 * kBF) / 64 - 1) * 64;
-        const int r = sgroup[k] + lane;
-        const Fp4View &W = r < TM ? p.a : (((r - TM) >> 5) & 1) ? p.u : p.b;
-        const int64_t rows = r < TM ? p.a.rows : p.N;
-        ssrc[k] = word_of(scale_row(r));
-        slast[k] = word_of(W.scales + (W.tile2d ? rows / 16 : rows) * ks - 1);
-    }
-    // the last slab's copies are held inside the operands
-    auto issue = [&](int64_t s, int stage) {
-        FwdStage<TM> &d = st[stage];
-        const int64_t at = s * 64;
-        if (s != nslab - 1) {
-#pragma unroll
-            for (int q = 0; q < RA; ++q) copy_at(abase + at, aoff[q], d.a + (wave * RA + q) * 1024);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) copy_at(bbase + at, boff[q], d.b + (wave * 2 + q) * 1024);
-#pragma unroll
-            for (int k = 0; k < SG; ++k)
-#pragma unroll
-                for (int w = 0; w < 3; ++w) copy_lds4(ssrc[k] + s * 8 + 4 * w, &d.sc[w][sgroup[k]]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < RA; ++q) copy_at(abase + at, held(aoff[q], aend - (abase + at)), d.a + (wave * RA + q) * 1024);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) copy_at(bbase + at, held(boff[q], bend - (bbase + at)), d.b + (wave * 2 + q) * 1024);
-#pragma unroll
-            for (int k = 0; k < SG; ++k)
-#pragma unroll
-                for (int w = 0; w < 3; ++w)
-                    copy_lds4(lesser(ssrc[k] + s * 8 + 4 * w, slast[k]), &d.sc[w][sgroup[k]]);
-        }
-    };
-
-    // the lane's fragment rows and the byte shift of their scales
-    const int h = lane >> 5, rl = lane & 31;
-    int sha[RA], shb[2];
-#pragma unroll
-    for (int i = 0; i < RA; ++i)
-        sha[i] = (int)(reinterpret_cast<uintptr_t>(scale_row(wm * (TM / 2) + i * 32 + rl)) & 3);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        shb[j] = (int)(reinterpret_cast<uintptr_t>(scale_row(TM + wn * 64 + j * 32 + rl)) & 3);
-
-    f32x16 acc[RA][2];
-#pragma unroll
-    for (int i = 0; i < RA; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{0};
-
-    const int64_t own = (nslab - grp + G - 1) / G;       // the group's slabs
-    for (int k = 0; k < AHEAD; ++k)
-        if (k < own) issue(k * G + grp, k);
-    int rd = 0, wr = AHEAD;                              // stages of its slab it and of slab it + AHEAD
-    for (int64_t it = 0; it < (nslab + G - 1) / G; ++it) {
-        if (it + AHEAD <= own) big::wait_vmcnt<(AHEAD - 1) * kIssued>();    // slab it has landed
-        else big::wait_vmcnt<0>();
-        __syncthreads();
-        const int64_t s = it * G + grp;
-        if (it + AHEAD < own) issue(s + AHEAD * G, wr);  // into the stage read before this barrier
-        FwdStage<TM> &d = st[rd];
-        rd = rd + 1 == NS ? 0 : rd + 1;
-        wr = wr + 1 == NS ? 0 : wr + 1;
-        uint32_t keep[2] = {~0u, ~0u};                   // scale bytes of blocks inside K
-        const bool last = tail && s == nslab - 1;
-        if (last) {
-            const int nb = tail / 16;
-            keep[0] = nb >= 4 ? ~0u : (1u << (8 * nb)) - 1;
-            keep[1] = nb <= 4 ? 0u : nb >= 8 ? ~0u : (1u << (8 * (nb - 4))) - 1;
-        }
-        if (tail % 32 && it == (nslab - 1) / G) {
-            // an operand's very last row ends in half a piece, which was copied
-            // from 8 bytes earlier: move it into place
-            const int c = tail / 32;
-            const int64_t col = p.N - 1 - n0;
-            const int64_t r = t == 0 ? p.a.rows - 1 - m0 : b_row((int)min(col, (int64_t)kBF)) + 32 * (t - 1);
-            if (last && (t == 0 ? r < TM : t <= 2 && col < kBF)) {
-                uint8_t *piece = (t == 0 ? d.a : d.b) + r * 64 + 16 * big::swz((int)r, c);
-                *reinterpret_cast<uint2 *>(piece) = *reinterpret_cast<const uint2 *>(piece + 8);
-            }
-            __syncthreads();
-        }
-        if (G > 1 && s >= nslab) continue;
-        uint32_t sa[RA][2], sb[2][2];
-        auto scales = [&](uint32_t (&o)[2], int row, int shift) {
-            const uint32_t w0 = d.sc[0][row], w1 = d.sc[1][row], w2 = d.sc[2][row];
-            o[0] = __builtin_amdgcn_alignbyte(w1, w0, shift) & keep[0];
-            o[1] = __builtin_amdgcn_alignbyte(w2, w1, shift) & keep[1];
-        };
-#pragma unroll
-        for (int i = 0; i < RA; ++i) scales(sa[i], wm * (TM / 2) + i * 32 + rl, sha[i]);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) scales(sb[j], TM + wn * 64 + j * 32 + rl, shb[j]);
-        uint4 ca[2][RA], cb[2][2];
-        f16x2 pa[2][RA], pb[2][2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-            for (int i = 0; i < RA; ++i) {
-                const int r = wm * (TM / 2) + i * 32 + rl;
-                ca[c][i] = *reinterpret_cast<const uint4 *>(d.a + r * 64 + 16 * big::swz(r, 2 * c + h));
-                pa[c][i] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sa[i][c] >> (16 * h), 1.0f, false);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = wn * 64 + j * 32 + rl;
-                cb[c][j] = *reinterpret_cast<const uint4 *>(d.b + r * 64 + 16 * big::swz(r, 2 * c + h));
-                pb[c][j] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(sb[j][c] >> (16 * h), 1.0f, false);
-            }
-        }
-        // eight MFMA steps; the operands of step k + 1 are expanded between the
-        // MFMAs of step k
-        f16x8 af[2][RA], bf[2][2];
-        auto expand = [&](int k) __attribute__((always_inline)) {
-            const int c = k >> 2, w = k & 3;
-#pragma unroll
-            for (int i = 0; i < RA; ++i) af[k & 1][i] = big::expand8_f16(big::word(ca[c][i], w), pa[c][i][w >> 1]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) bf[k & 1][j] = big::expand8_f16(big::word(cb[c][j], w), pb[c][j][w >> 1]);
-        };
-        expand(0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (k < 7) expand(k + 1);
-#pragma unroll
-            for (int i = 0; i < RA; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(bf[k & 1][j], af[k & 1][i], acc[i][j], 0, 0, 0);
-#pragma unroll
-            for (int m = 0; m < 2 * RA; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, (RA + 2) * 8 / (2 * RA), 0);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-
-    join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[RA * 32]>(acc));
-    if (grp) return;
-    const float sg = p.b.s_dec[0], su = p.u.s_dec[0];
-    const int64_t n = n0 + wn * 32 + 16 * h;               // the lane's first column
-#pragma unroll
-    for (int i = 0; i < RA; ++i) {
-        const int64_t m = m0 + wm * (TM / 2) + i * 32 + rl;
-        const float sa = p.a.s_dec[p.a.sdec_rows ? (m < p.M ? m : p.M - 1) : 0];
-        f32x16 g = acc[i][0], u = acc[i][1];
-        scale16(g, sa * sg);
-        scale16(u, sa * su);
-        const bool in = m < p.M && n < p.N;
-        if (p.g_codes) {
-            uint32_t wg[4], wu[4];
-            const uint32_t bg = checkpoint16(g, wg), bu = checkpoint16(u, wu);
-            if (in) {
-                *reinterpret_cast<uint4 *>(p.g_codes + m * p.N + n) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
-                *reinterpret_cast<uint4 *>(p.u_codes + m * p.N + n) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-                if (h == 0) {
-                    p.g_scales[m * (p.N / 32) + n / 32] = (uint8_t)bg;
-                    p.u_scales[m * (p.N / 32) + n / 32] = (uint8_t)bu;
+        for (int i = 0; i < RA; ++i) {
+            const int64_t m = mw + i * 32 + rl;
+            const float sa = p.a.s_dec[p.a.sdec_rows ? (m < p.M ? m : p.M - 1) : 0];
+            f32x16 g = acc[i][0], u = acc[i][1];
+            scale16(g, sa * sg);
+            scale16(u, sa * su);
+            const bool in = m < p.M && n < p.N;
+            if (p.g_codes) {
+                uint32_t wg[4], wu[4];
+                const uint32_t bg = checkpoint16(g, wg), bu = checkpoint16(u, wu);
+                if (in) {
+                    *reinterpret_cast<uint4 *>(p.g_codes + m * p.N + n) = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+                    *reinterpret_cast<uint4 *>(p.u_codes + m * p.N + n) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+                    if (h == 0) {
+                        p.g_scales[m * (p.N / 32) + n / 32] = (uint8_t)bg;
+                        p.u_scales[m * (p.N / 32) + n / 32] = (uint8_t)bu;
+                    }
                 }
             }
-        }
-        if (!in) continue;
+            if (!in) continue;
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-            float y[2][4];
+            for (int q = 0; q < 4; q += 2) {
+                float y[2][4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
-            store8<BF16_OUT>(p.h, m * p.ldh + n + 4 * q, y[0], y[1]);
+                for (int e = 0; e < 8; ++e) y[e >> 2][e & 3] = gate_act<ACT, BF16_OUT>(g[4 * q + e]) * u[4 * q + e];
+                store8<BF16_OUT>(p.h, m * p.ldh + n + 4 * q, y[0], y[1]);
+            }
         }
-    }
+    };
+    run_tile<TM, NS, G, GatedSide>(smem, p, finish);
 }
 
 // ---------------------------------------------------------------------------
@@ -529,26 +267,10 @@ __global__ __launch_bounds__(kThreads * G) void gated_bwd_kernel(GatedBwdParams 
     }
 }
 
-// Launch with dynamic LDS; the kernel's limit is raised once per kernel.
-template <auto Kernel, typename Params>
-hipError_t launch(int64_t tiles, int threads, size_t shm, const Params &p, hipStream_t s) {
-    if (tiles * threads > UINT32_MAX) return hipErrorInvalidConfiguration;    // would be cut off
-    static const bool attr_set = [shm] {
-        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel),
-                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
-        return true;
-    }();
-    (void)attr_set;
-    hipLaunchKernelGGL(Kernel, dim3((unsigned)tiles), dim3((unsigned)threads), shm, s, p);
-    return hipGetLastError();
-}
-
-int64_t tiles_of(int64_t M, int64_t N, int tm, int tn) { return ((M + tm - 1) / tm) * ((N + tn - 1) / tn); }
-
 template <int TM, int NS, int G>
 hipError_t fwd(const GatedParams &p, int act, bool bf16_out, hipStream_t s) {
-    const int64_t tiles = tiles_of(p.M, p.N, TM, kBF);
-    constexpr size_t shm = G * NS * sizeof(FwdStage<TM>);
+    const int64_t tiles = tiles_of(p.M, p.N, TM, GatedSide::kCols);
+    constexpr size_t shm = G * NS * sizeof(small::Stage<TM>);
     if (act == kActGelu)
         return bf16_out ? launch<gated_gemm_kernel<TM, NS, G, kActGelu, true>>(tiles, kThreads * G, shm, p, s)
                         : launch<gated_gemm_kernel<TM, NS, G, kActGelu, false>>(tiles, kThreads * G, shm, p, s);
@@ -583,8 +305,8 @@ hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipSt
     auto al8 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 8 == 0; };
     const bool large = p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales) && al8(p.u.scales);
     const int64_t cus = device_cus(s);
-    if (tiles_of(p.M, p.N, 64, kBF) <= cus) return fwd<64, 2, 4>(p, act, bf16_out, s);
-    if (tiles_of(p.M, p.N, 128, kBF) <= cus) return fwd<128, 3, 2>(p, act, bf16_out, s);
+    if (tiles_of(p.M, p.N, 64, GatedSide::kCols) <= cus) return fwd<64, 2, 4>(p, act, bf16_out, s);
+    if (tiles_of(p.M, p.N, 128, GatedSide::kCols) <= cus) return fwd<128, 3, 2>(p, act, bf16_out, s);
     if (large) return launch_gated_gemm_big(p, act, bf16_out, s);
     return fwd<256, 2, 1>(p, act, bf16_out, s);
 }
