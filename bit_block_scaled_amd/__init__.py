@@ -20,9 +20,10 @@ BBS_OK, BBS_EINVAL, BBS_ENOTSUP, BBS_EHIP = 0, -1, -2, -3
 RTN, SR = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
 FMT_NVFP4, FMT_MXFP8, FMT_MXFP4 = 0, 1, 2
-ACT_SILU, ACT_GELU = 0, 1
+ACT_SILU, ACT_GELU, ACT_NONE = 0, 1, 2
 AMAX_WS_FLOATS = 11264
 GEMV_MAX_TOKENS = 64
+BIAS_PARTS = 64
 
 
 class Fp4Desc(C.Structure):
@@ -103,7 +104,11 @@ def _load():
                                          C.POINTER(Mx8Desc), i32, vp, vp, i32, i64, vp]
     lib.nvfp4_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i64, vp]
     lib.nvfp4_gated_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, vp, i32, i64, vp]
-    for f in ("nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
+    lib.nvfp4_gemm_bias_act.argtypes = [C.POINTER(Fp4Desc), C.POINTER(Fp4Desc), vp, i32, i32, vp, i64,
+                                        C.POINTER(Mx8Desc), vp, i32, i64, vp]
+    lib.mxfp8_bias_act_bwd.argtypes = [vp, i64, i64, i64, C.POINTER(Mx8Desc), i32, vp, i64, vp, i32, vp, vp]
+    lib.nvfp4_gemv_bias_act.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, i64, vp, i32, i64, vp]
+    for f in ("nvfp4_gemm_bias_act", "mxfp8_bias_act_bwd", "nvfp4_gemv_bias_act", "nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
               "nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_requantize_t", "nvfp4_gemm", "grouped_nvfp4_gemm",
               "s2f6_quantize", "s2f6_combine", "mxfp4_quantize", "nvfp4_gemm_quant",
               "grouped_nvfp4_gemm_quant", "nvfp4_gemm_s2f6", "grouped_nvfp4_gemm_s2f6"):
@@ -467,5 +472,89 @@ def nvfp4_gated_gemv(fmt, x, Wg, Wu, h, h_dtype, act=ACT_SILU, ldh=None, stream=
     T, ldx, ldh, s = _few_tokens(fmt, x, Wg, Wu, h, h_dtype, ldh, stream)
     status = lib.nvfp4_gated_gemv(fmt, x.data_ptr(), T, ldx, Wg.packed(), Wu.packed(), act, h.data_ptr(),
                                   h_dtype, ldh, s)
+    if status:
+        _check(status)
+
+
+# A linear layer's bias and residual come as tensors; the type of a bias is its own.
+
+_TYPES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
+def _vector(t, n, name):
+    """(pointer, type) of n adjacent float32 or bfloat16 values."""
+    if t is None:
+        return None, OUT_F32
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1) or t.dtype not in _TYPES:
+        raise ValueError(f"{name} must hold {n} adjacent float32 or bfloat16 values")
+    return t.data_ptr(), _TYPES[t.dtype]
+
+
+def _mx8_shape(t, rows, cols, name):
+    """An MXFP8Tensor's sizes, against its own tensors."""
+    if not isinstance(t, MXFP8Tensor) or (t.rows, t.cols) != (rows, cols):
+        raise ValueError(f"{name} must be an MXFP8Tensor of {rows} x {cols}")
+
+
+def nvfp4_gemm_bias_act(A, B, out, out_dtype, bias=None, act=ACT_NONE, residual=None, z_ckpt=None, ldo=None,
+                        ldr=None, stream=None):
+    """out = act(A * B^T + bias) + residual in one kernel (NVFP4Tensors A [M, K], B
+    [N, K]; bias [N] float32 or bfloat16; residual [M, N] of out's type, out itself
+    allowed); z_ckpt (MXFP8Tensor [M, N]) receives the 8-bit checkpoint of A * B^T
+    + bias for mxfp8_bias_act_bwd."""
+    M, N = A.rows, B.rows
+    ldo = _output_ld(out, out_dtype, M, N, ldo, "out")
+    if residual is not None:
+        ldr = _output_ld(residual, out_dtype, M, N, ldr, "residual")
+    b, b_dtype = _vector(bias, N, "bias")
+    if z_ckpt is not None:
+        _mx8_shape(z_ckpt, M, N, "z_ckpt")
+    more = [t for t in (bias, residual) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
+    s = _on_current(stream, A.codes, B.codes, out, *more)
+    ad, bd = A.desc(), B.desc()
+    zd = z_ckpt.desc() if z_ckpt is not None else None
+    _check(lib.nvfp4_gemm_bias_act(C.byref(ad), C.byref(bd), b, b_dtype, act, _ptr(residual), ldr or 0,
+                                   C.byref(zd) if zd is not None else None, _ptr(out), out_dtype, ldo, s))
+
+
+def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=None):
+    """Backward pass of act(z) + residual, z = product + bias, from the 8-bit
+    checkpoint of z: dZ = dY * act'(z) and dbias = its sum over the rows.  dY and dZ:
+    BF16 patterns [M, N] (dZ may be dY); dbias: [N] float32 or bfloat16; z_ckpt is
+    not read, and may be None, with ACT_NONE.  ws: BIAS_PARTS * N float32 of
+    workspace for dbias (allocated if None)."""
+    M, N = dY.shape
+    ldy = _output_ld(dY, OUT_BF16, M, N, None, "dY")
+    ldz = _output_ld(dZ, OUT_BF16, M, N, None, "dZ") if dZ is not None else 0
+    if z_ckpt is not None:
+        _mx8_shape(z_ckpt, M, N, "z_ckpt")
+    elif act != ACT_NONE:
+        raise ValueError("an activation's backward pass needs z_ckpt")
+    b, b_dtype = _vector(dbias, N, "dbias")
+    if dbias is not None:
+        if ws is None:
+            ws = torch.empty((BIAS_PARTS * N,), dtype=torch.float32, device=dY.device)
+        elif ws.dtype != torch.float32 or not ws.is_contiguous() or ws.numel() < BIAS_PARTS * N:
+            raise ValueError(f"ws must hold {BIAS_PARTS * N} adjacent float32 values")
+    more = [t for t in (dZ, dbias, ws) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
+    s = _on_current(stream, dY, *more)
+    zd = z_ckpt.desc() if z_ckpt is not None else None
+    _check(lib.mxfp8_bias_act_bwd(_ptr(dY), M, N, ldy, C.byref(zd) if zd is not None else None, act, _ptr(dZ), ldz,
+                                  b, b_dtype, _ptr(ws), s))
+
+
+def nvfp4_gemv_bias_act(fmt, x, W, y, y_dtype, bias=None, act=ACT_NONE, residual=None, ldy=None, ldr=None,
+                        stream=None):
+    """y = act(x * W^T + bias) + residual for 1 to GEMV_MAX_TOKENS tokens, x, W and y
+    as nvfp4_gemv; bias [N] float32 or bfloat16, residual [T, N] of y's type (y
+    itself allowed)."""
+    T, ldx, ldy, s = _few_tokens(fmt, x, W, W, y, y_dtype, ldy, stream)
+    b, b_dtype = _vector(bias, W.rows, "bias")
+    if residual is not None:
+        ldr = _output_ld(residual, y_dtype, T, W.rows, ldr, "residual")
+    if any(t is not None and t.get_device() != x.get_device() for t in (bias, residual)):
+        raise ValueError("the tensors must be on one GPU")
+    status = lib.nvfp4_gemv_bias_act(fmt, x.data_ptr(), T, ldx, W.packed(), b, b_dtype, act, _ptr(residual), ldr or 0,
+                                     y.data_ptr(), y_dtype, ldy, s)
     if status:
         _check(status)

@@ -10,6 +10,7 @@
 #include "../../include/bbs.h"
 #include "bbs_kernels.hpp"
 #include "gated.hpp"
+#include "linear.hpp"
 
 static_assert(bbs::kWorkspaceFloats == BBS_AMAX_WS_FLOATS, "workspace size mismatch");
 
@@ -692,10 +693,29 @@ int check_tiles(int64_t M, int64_t N, int64_t TM, int64_t TN) {
     return BBS_OK;
 }
 
-// Shared checks of nvfp4_gemv (Wu null) and nvfp4_gated_gemv.
+bool any_act_ok(int32_t act) { return act_ok(act) || act == BBS_ACT_NONE; }
+static_assert(bbs::kActNone == BBS_ACT_NONE && bbs::kBiasParts == BBS_BIAS_PARTS, "linear layer's constants");
+
+// A bias of `cols` values, read `align` bytes at a time (0: value by value).
+int check_bias(const void *b, int32_t dtype, uintptr_t align) {
+    if (!b) return BBS_OK;
+    if (!dtype_ok(dtype)) return fail(BBS_EINVAL, "bad bias_dtype");
+    if (!aligned(b, align ? align : dtype == BBS_OUT_BF16 ? 2 : 4)) return fail(BBS_EINVAL, "bias not aligned");
+    return BBS_OK;
+}
+
+// What nvfp4_gemv_bias_act adds to a product.
+struct GemvEpilogue {
+    const void *bias;
+    int32_t bias_dtype, act;
+    const void *residual;
+    int64_t ldr;
+};
+
+// Shared checks of nvfp4_gemv, nvfp4_gemv_bias_act (Wu null) and nvfp4_gated_gemv.
 int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
-              const void *Wu, bool gated, int32_t act, void *y, int32_t y_dtype, int64_t ldy,
-              void *stream) {
+              const void *Wu, bool gated, int32_t act, const GemvEpilogue &epi, void *y, int32_t y_dtype,
+              int64_t ldy, void *stream) {
     int st;
     if (!x) return fail(BBS_EINVAL, "null x");
     if (!y) return fail(BBS_EINVAL, "null y");
@@ -735,6 +755,15 @@ int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const
     if (!aligned(x, 16)) return fail(BBS_EINVAL, "x not 16-byte aligned");
     if (ldy < p.N) return fail(BBS_EINVAL, "output row stride < N");
     if (!aligned(y, y_dtype == BBS_OUT_BF16 ? 2 : 4)) return fail(BBS_EINVAL, "y not aligned to its type");
+    if ((st = check_bias(epi.bias, epi.bias_dtype, 0))) return st;
+    if (epi.residual && epi.ldr < p.N) return fail(BBS_EINVAL, "residual row stride < N");
+    if (!aligned(epi.residual, y_dtype == BBS_OUT_BF16 ? 2 : 4))
+        return fail(BBS_EINVAL, "residual not aligned to its type");
+    p.bias = epi.bias;
+    p.bias_bf16 = epi.bias_dtype == BBS_OUT_BF16;
+    p.epi_act = epi.act;
+    p.r = epi.residual;
+    p.ldr = epi.ldr;
     // row offsets inside a workgroup's 64 rows are 32 bits wide
     if (p.N > INT32_MAX || p.K > (int64_t)1 << 26)
         return fail(BBS_ENOTSUP, "weights of more than 2^31 - 1 rows or 2^26 columns");
@@ -754,14 +783,25 @@ int gemv_impl(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const
 int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W, void *y,
                int32_t y_dtype, int64_t ldy, void *stream) {
     g_err[0] = 0;
-    return gemv_impl(fmt, x, tokens, ldx, W, nullptr, false, 0, y, y_dtype, ldy, stream);
+    return gemv_impl(fmt, x, tokens, ldx, W, nullptr, false, 0, {nullptr, 0, BBS_ACT_NONE, nullptr, 0}, y, y_dtype,
+                     ldy, stream);
+}
+
+int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
+                        const void *bias, int32_t bias_dtype, int32_t act, const void *residual, int64_t ldr,
+                        void *y, int32_t y_dtype, int64_t ldy, void *stream) {
+    g_err[0] = 0;
+    if (!any_act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    return gemv_impl(fmt, x, tokens, ldx, W, nullptr, false, 0, {bias, bias_dtype, act, residual, ldr}, y, y_dtype,
+                     ldy, stream);
 }
 
 int nvfp4_gated_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *Wg,
                      const void *Wu, int32_t act, void *h, int32_t h_dtype, int64_t ldh,
                      void *stream) {
     g_err[0] = 0;
-    return gemv_impl(fmt, x, tokens, ldx, Wg, Wu, true, act, h, h_dtype, ldh, stream);
+    return gemv_impl(fmt, x, tokens, ldx, Wg, Wu, true, act, {nullptr, 0, BBS_ACT_NONE, nullptr, 0}, h, h_dtype, ldh,
+                     stream);
 }
 
 int nvfp4_gated_gemm(const bbs_fp4 *A, const bbs_fp4 *Wg, const bbs_fp4 *Wu, int32_t act, void *H,
@@ -843,6 +883,80 @@ int mxfp8_gemm_gated_bwd(const bbs_mx8 *dY, const bbs_mx8 *Wt, const bbs_mx8 *g8
     return hip_status(bbs::launch_gated_bwd(p, act, dtype == BBS_OUT_BF16,
                                             reinterpret_cast<hipStream_t>(stream)),
                       "gated backward launch");
+}
+
+int nvfp4_gemm_bias_act(const bbs_fp4 *A, const bbs_fp4 *B, const void *bias, int32_t bias_dtype, int32_t act,
+                        const void *residual, int64_t ldr, const bbs_mx8 *z8, void *C, int32_t c_dtype,
+                        int64_t ldc, void *stream) {
+    g_err[0] = 0;
+    int st;
+    if ((st = check_fp4(A, "A", true))) return st;
+    if ((st = check_fp4(B, "B", true))) return st;
+    if (!any_act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (A->cols != B->cols) return fail(BBS_EINVAL, "A.cols != B.cols");
+    if (B->sdec_per_row) return fail(BBS_ENOTSUP, "B with a per-row decode scale");
+    // row offsets inside a tile are 32 bits wide
+    if (A->cols >= (int64_t)1 << 25) return fail(BBS_ENOTSUP, "2^25 columns or more");
+    if ((st = check_tiles(A->rows, B->rows, 256, 128))) return st;
+    if ((st = check_rows_out(C, c_dtype, B->rows, ldc, "C"))) return st;
+    if ((st = check_bias(bias, bias_dtype, 16))) return st;
+    if (residual && (st = check_rows_out(residual, c_dtype, B->rows, ldr, "residual"))) return st;
+    bbs::LinearParams p{};
+    if (z8) {
+        if ((st = check_mx8(z8, "z8"))) return st;
+        if (z8->rows != A->rows || z8->cols != B->rows) return fail(BBS_EINVAL, "z8 must be A.rows x B.rows");
+        p.z_codes = z8->codes;
+        p.z_scales = z8->scales;
+    }
+    p.a = {A->codes, A->scales, A->s_dec, A->rows, A->tile2d, A->sdec_per_row};
+    p.b = {B->codes, B->scales, B->s_dec, B->rows, B->tile2d, 0};
+    p.M = A->rows;
+    p.N = B->rows;
+    p.K = A->cols;
+    p.c = C;
+    p.ldc = ldc;
+    p.bias = bias;
+    p.bias_bf16 = bias_dtype == BBS_OUT_BF16;
+    p.act = act;
+    p.r = residual;
+    p.ldr = ldr;
+    return hip_status(bbs::launch_linear(p, c_dtype == BBS_OUT_BF16, reinterpret_cast<hipStream_t>(stream)),
+                      "linear launch");
+}
+
+int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t ldy, const bbs_mx8 *z8, int32_t act,
+                       uint16_t *dZ, int64_t ldz, void *dbias, int32_t dbias_dtype, float *ws, void *stream) {
+    g_err[0] = 0;
+    int st;
+    if (!any_act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (rows <= 0 || cols <= 0 || cols % 16) return fail(BBS_EINVAL, "rows and cols must be positive, cols %% 16 == 0");
+    // rows of a launch's ranges, columns of its grid
+    if (rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31) return fail(BBS_ENOTSUP, "2^31 rows or columns or more");
+    if ((st = check_rows_out(dY, BBS_OUT_BF16, cols, ldy, "dY"))) return st;
+    if (dZ && (st = check_rows_out(dZ, BBS_OUT_BF16, cols, ldz, "dZ"))) return st;
+    if (!dZ && !dbias) return fail(BBS_EINVAL, "neither dZ nor dbias");
+    bbs::BiasActBwdParams p{};
+    if (act != BBS_ACT_NONE) {
+        if ((st = check_mx8(z8, "z8"))) return st;
+        if (z8->rows != rows || z8->cols != cols) return fail(BBS_EINVAL, "z8 must have dY's shape");
+        p.z_codes = z8->codes;
+        p.z_scales = z8->scales;
+    }
+    if (dbias) {
+        if ((st = check_bias(dbias, dbias_dtype, 0))) return st;
+        if (!ws || !aligned(ws, 4)) return fail(BBS_EINVAL, "dbias needs a workspace");
+    }
+    p.dy = dY;
+    p.M = rows;
+    p.N = cols;
+    p.ldy = ldy;
+    p.act = act;
+    p.dz = dZ;
+    p.ldz = ldz;
+    p.db = dbias;
+    p.db_bf16 = dbias_dtype == BBS_OUT_BF16;
+    p.part = ws;
+    return hip_status(bbs::launch_bias_act_bwd(p, reinterpret_cast<hipStream_t>(stream)), "bias backward launch");
 }
 
 }  // extern "C"

@@ -11,7 +11,7 @@
 
 namespace bbs {
 
-constexpr int kActSilu = 0, kActGelu = 1;
+constexpr int kActSilu = 0, kActGelu = 1, kActNone = 2;
 
 // Forward: NVFP4 operands (b = the gate weights, u = the up weights of the
 // same shape and layout), output h, optional MXFP8 checkpoints of g and u.
@@ -45,6 +45,12 @@ struct GemvParams {
     int64_t ldy;
     int bf16_out;
     int act;                       // < 0: one matrix, y = x W^T; else the gated form of the two
+    // one matrix: y = epi_act(x W^T + bias) + r
+    const void *bias;              // N values, or null
+    int bias_bf16;
+    int epi_act;
+    const void *r;                 // residual of y's type, or null
+    int64_t ldr;
 };
 
 hipError_t launch_gated_gemm(const GatedParams &p, int act, bool bf16_out, hipStream_t s);

@@ -47,14 +47,24 @@ constexpr int kRows16 = 0;       // NVFP4, one E4M3 byte per 16 weights of a row
 constexpr int kTiles16 = 1;      // NVFP4, one E4M3 byte per 16 x 16 weights
 constexpr int kRows32 = 2;       // MXFP4, one E8M0 byte per 32 weights of a row
 
-// One output from its sums: decode scales, activation, one rounding.  The
-// activation and the output type are the same for every lane.
+// Value n of an array of FP32 values or BF16 patterns.
+__device__ __forceinline__ float value_at(const void *p, int64_t n, int bf16) {
+    return bf16 ? bf16_to_f32(static_cast<const uint16_t *>(p)[n]) : static_cast<const float *>(p)[n];
+}
+
+// One output from its sums: decode scales, bias, activation, residual, one
+// rounding.  Which of these apply and the types are the same for every lane.
 template <int SC, int NM>
 __device__ __forceinline__ void finish(const GemvParams &p, int64_t t, int64_t n, const float (&v)[2]) {
     float y = SC == kRows32 ? v[0] : v[0] * p.w.s_dec[0];
     if constexpr (NM == 2) {
         const float u = SC == kRows32 ? v[1] : v[1] * p.u.s_dec[0];
         y = (p.act == kActSilu ? gate_act<kActSilu, false>(y) : gate_act<kActGelu, false>(y)) * u;
+    } else {
+        if (p.bias) y += value_at(p.bias, n, p.bias_bf16);
+        if (p.epi_act == kActSilu) y = gate_act<kActSilu, false>(y);
+        else if (p.epi_act == kActGelu) y = gate_act<kActGelu, false>(y);
+        if (p.r) y += value_at(p.r, t * p.ldr + n, p.bf16_out);
     }
     if (p.bf16_out) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(y, y);
     else static_cast<float *>(p.y)[t * p.ldy + n] = y;
@@ -620,6 +630,8 @@ hipError_t launch_gemv(const GemvParams &p, bool mxfp4, hipStream_t s) {
     for (int64_t n = 0; n < p.N; n += kRows) {
         q.N = std::min(kRows, p.N - n);
         q.y = static_cast<uint8_t *>(p.y) + n * (p.bf16_out ? 2 : 4);
+        if (p.bias) q.bias = static_cast<const uint8_t *>(p.bias) + n * (p.bias_bf16 ? 2 : 4);
+        if (p.r) q.r = static_cast<const uint8_t *>(p.r) + n * (p.bf16_out ? 2 : 4);
         for (auto w : {&GemvParams::w, &GemvParams::u}) {
             if (p.act < 0 && w == &GemvParams::u) continue;
             (q.*w).codes = (p.*w).codes + n * (p.K / 2);

@@ -1,0 +1,221 @@
+// A linear layer's NVFP4 product with bias, activation and residual, small-tile
+// kernel for any K the format allows (gfx950), the choice between it and the
+// large-tile kernel, and the backward pass of the bias and the activation.
+//
+//   forward   z = A W^T + b (NVFP4 x NVFP4), c = act(z) + r, optionally the MXFP8
+//             checkpoint of z
+//   backward  dz = dy * act'(z), db = sum over the rows of dz, with z read back
+//             from the checkpoint
+#include "gemm_nvfp4_small.hpp"
+#include "linear.hpp"
+
+namespace bbs {
+
+namespace {
+
+using small::kThreads;
+using small::launch, small::run_tile, small::tiles_of;
+using small::PlainSide;
+
+// ---------------------------------------------------------------------------
+// Forward: TM rows by 128 columns.
+// ---------------------------------------------------------------------------
+template <int TM, int NS, int G, bool BF16_OUT>
+__global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void linear_kernel(LinearParams p) {
+    constexpr int RA = TM / 64;                    // 32-row blocks of a wave
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto finish = [](const LinearParams &p, const f32x16 (&acc)[RA][2], int64_t mw, int64_t n0, int wn, int lane)
+                      __attribute__((always_inline)) {
+        const int h = lane >> 5, rl = lane & 31;
+        const float sb = p.b.s_dec[0];
+#pragma unroll
+        for (int i = 0; i < RA; ++i) {
+            const int64_t m = mw + i * 32 + rl;
+            const float scale = p.a.s_dec[p.a.sdec_rows ? (m < p.M ? m : p.M - 1) : 0] * sb;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t n = n0 + wn * 64 + j * 32 + 16 * h;   // the lane's first column
+                const bool in = m < p.M && n < p.N;
+                f32x16 v = acc[i][j];
+                scale16(v, scale);
+                if (p.bias) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float b[4];
+                        load_bias4(p.bias, p.bias_bf16, n < p.N ? n + 4 * q : 0, b);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[4 * q + e] = v[4 * q + e] + b[e];
+                    }
+                }
+                if (p.z_codes) {
+                    uint32_t w[4];
+                    const uint32_t byte = checkpoint16(v, w);
+                    if (in) {
+                        *reinterpret_cast<uint4 *>(p.z_codes + m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (h == 0) p.z_scales[m * (p.N / 32) + n / 32] = (uint8_t)byte;
+                    }
+                }
+                if (!in) continue;
+                act_all<BF16_OUT, 16>(v, p.act);
+                if (p.r) {
+                    const int64_t at = m * p.ldr + n;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float r[4];
+                        load_bias4(p.r, BF16_OUT, at + 4 * q, r);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[4 * q + e] = v[4 * q + e] + r[e];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    const float y0[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                    const float y1[4] = {v[4 * q + 4], v[4 * q + 5], v[4 * q + 6], v[4 * q + 7]};
+                    store8<BF16_OUT>(p.c, m * p.ldc + n + 4 * q, y0, y1);
+                }
+            }
+        }
+    };
+    run_tile<TM, NS, G, PlainSide>(smem, p, finish);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: a workgroup takes 128 columns of a range of rows, sixteen lanes to
+// a row, eight columns a lane; column sums stay in registers over the rows and
+// are joined in LDS.  The sums of the ranges go to memory and a second kernel
+// adds them in order, so a call's bits do not depend on the order in which
+// workgroups run.
+// ---------------------------------------------------------------------------
+constexpr int kBwdCols = 128, kBwdRows = 16;       // rows of one step of a workgroup
+constexpr int kBwdDeep = 4;                        // steps whose loads are in flight together
+
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = __uint_as_float(w[e] << 16);
+        f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_db(void *db, int64_t n, float v) {
+    if (BF16) static_cast<uint16_t *>(db)[n] = (uint16_t)pk_bf16(v, v);
+    else static_cast<float *>(db)[n] = v;
+}
+
+// DEEP steps from row m on; rows past `end` add nothing.
+template <int ACT, int DEEP>
+__device__ __forceinline__ void bwd_rows(const BiasActBwdParams &p, int64_t m, int64_t end, int64_t n,
+                                         float (&sum)[8]) {
+    uint4 dy[DEEP];
+    uint2 z[DEEP];
+    uint32_t zs[DEEP];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+        const int64_t r = min(m + d * kBwdRows, end - 1);
+        dy[d] = *reinterpret_cast<const uint4 *>(p.dy + r * p.ldy + n);
+        if (ACT != kActNone) {
+            z[d] = *reinterpret_cast<const uint2 *>(p.z_codes + r * p.N + n);
+            zs[d] = p.z_scales[r * (p.N / 32) + n / 32];
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+        const int64_t r = m + d * kBwdRows;
+        float v[8];
+        unpack8(dy[d], v);
+        if (ACT != kActNone) {
+            float zv[8];
+            decode4(z[d].x, zs[d], reinterpret_cast<float(&)[4]>(zv[0]));
+            decode4(z[d].y, zs[d], reinterpret_cast<float(&)[4]>(zv[4]));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float slope;
+                gate_act_grad<ACT == kActNone ? kActSilu : ACT, true>(zv[e], slope);
+                v[e] = v[e] * slope;
+            }
+        }
+        if (r >= end) break;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
+        if (p.dz)
+            *reinterpret_cast<uint4 *>(p.dz + r * p.ldz + n) =
+                make_uint4(pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]), pk_bf16(v[6], v[7]));
+    }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void bias_act_bwd_kernel(BiasActBwdParams p, int64_t rows, int parts) {
+    __shared__ float part[kBwdRows][kBwdCols];
+    const int t = threadIdx.x, rl = t >> 4, c = (t & 15) * 8;
+    const int64_t n = (int64_t)blockIdx.x * kBwdCols + c;
+    const int64_t m0 = (int64_t)blockIdx.y * rows, end = min(m0 + rows, p.M);
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (n < p.N)
+        for (int64_t m = m0 + rl; m < end; m += kBwdRows * kBwdDeep) bwd_rows<ACT, kBwdDeep>(p, m, end, n, sum);
+    if (!p.db) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[rl][c + e] = sum[e];
+    __syncthreads();
+    const int64_t nc = (int64_t)blockIdx.x * kBwdCols + t;
+    if (t < kBwdCols && nc < p.N) {
+        float v = part[0][t];
+#pragma unroll
+        for (int r = 1; r < kBwdRows; ++r) v += part[r][t];
+        if (parts > 1) p.part[(int64_t)blockIdx.y * p.N + nc] = v;
+        else if (p.db_bf16) store_db<true>(p.db, nc, v);
+        else store_db<false>(p.db, nc, v);
+    }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(64) void bias_sum_kernel(const float *part, int64_t N, int parts, void *db) {
+    const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (n >= N) return;
+    float v = part[n];
+    for (int i = 1; i < parts; ++i) v += part[i * N + n];
+    store_db<BF16>(db, n, v);
+}
+
+template <int TM, int NS, int G>
+hipError_t fwd(const LinearParams &p, bool bf16_out, hipStream_t s) {
+    const int64_t tiles = tiles_of(p.M, p.N, TM, PlainSide::kCols);
+    constexpr size_t shm = G * NS * sizeof(small::Stage<TM>);
+    return bf16_out ? launch<linear_kernel<TM, NS, G, true>>(tiles, kThreads * G, shm, p, s)
+                    : launch<linear_kernel<TM, NS, G, false>>(tiles, kThreads * G, shm, p, s);
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinearParams &p, bool bf16_out, hipStream_t s) {
+    auto al8 = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 8 == 0; };
+    const bool large = p.K % 128 == 0 && al8(p.a.scales) && al8(p.b.scales);
+    const int64_t cus = device_cus(s);
+    if (tiles_of(p.M, p.N, 64, PlainSide::kCols) <= cus) return fwd<64, 2, 4>(p, bf16_out, s);
+    if (tiles_of(p.M, p.N, 128, PlainSide::kCols) <= cus) return fwd<128, 3, 2>(p, bf16_out, s);
+    if (large) return launch_linear_big(p, bf16_out, s);
+    return fwd<256, 2, 1>(p, bf16_out, s);
+}
+
+hipError_t launch_bias_act_bwd(const BiasActBwdParams &p, hipStream_t s) {
+    const int64_t cols = (p.N + kBwdCols - 1) / kBwdCols;
+    const int64_t most = (p.M + kBwdRows - 1) / kBwdRows;
+    int64_t parts = (8 * device_cus(s) + cols - 1) / cols;
+    parts = parts > kBiasParts ? kBiasParts : parts;
+    parts = parts > most ? most : parts;
+    const int64_t rows = ((p.M + parts - 1) / parts + kBwdRows - 1) / kBwdRows * kBwdRows;
+    parts = (p.M + rows - 1) / rows;
+    const dim3 grid((unsigned)cols, (unsigned)parts);
+    if (p.act == kActSilu) hipLaunchKernelGGL((bias_act_bwd_kernel<kActSilu>), grid, dim3(256), 0, s, p, rows, (int)parts);
+    else if (p.act == kActGelu) hipLaunchKernelGGL((bias_act_bwd_kernel<kActGelu>), grid, dim3(256), 0, s, p, rows, (int)parts);
+    else hipLaunchKernelGGL((bias_act_bwd_kernel<kActNone>), grid, dim3(256), 0, s, p, rows, (int)parts);
+    if (p.db && parts > 1) {
+        const dim3 g2((unsigned)((p.N + 63) / 64));
+        if (p.db_bf16) hipLaunchKernelGGL(bias_sum_kernel<true>, g2, dim3(64), 0, s, p.part, p.N, (int)parts, p.db);
+        else hipLaunchKernelGGL(bias_sum_kernel<false>, g2, dim3(64), 0, s, p.part, p.N, (int)parts, p.db);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace bbs

@@ -47,11 +47,15 @@ enum bbs_out_dtype { BBS_OUT_F32 = 0, BBS_OUT_BF16 = 1 };
 enum bbs_fmt { BBS_FMT_NVFP4 = 0, BBS_FMT_MXFP8 = 1, BBS_FMT_MXFP4 = 2 };
 /* Activation of a gated feed-forward block, act(g) = g * sigma(z), sigma(z) =
  * 1 / (1 + e^-z): SiLU has z = g; GELU (tanh form) has
- * z = 2 sqrt(2/pi) (g + 0.044715 g^3). */
-enum bbs_act { BBS_ACT_SILU = 0, BBS_ACT_GELU = 1 };
+ * z = 2 sqrt(2/pi) (g + 0.044715 g^3).  BBS_ACT_NONE, act(g) = g, is for the
+ * calls that name it. */
+enum bbs_act { BBS_ACT_SILU = 0, BBS_ACT_GELU = 1, BBS_ACT_NONE = 2 };
 
 /* Most tokens nvfp4_gemv and nvfp4_gated_gemv take in one call. */
 #define BBS_GEMV_MAX_TOKENS 64
+
+/* mxfp8_bias_act_bwd needs up to this many floats of device workspace a column. */
+#define BBS_BIAS_PARTS 64
 
 /* Words of device workspace nvfp4_quantize needs for its amax partials. */
 #define BBS_AMAX_WS_FLOATS 11264
@@ -395,6 +399,49 @@ int nvfp4_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, cons
 int nvfp4_gated_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *Wg,
                      const void *Wu, int32_t act, void *h, int32_t h_dtype, int64_t ldh,
                      void *stream);
+
+/* A linear layer in one kernel: with z = A * B^T + bias (the product as
+ * nvfp4_gemm, in FP32),
+ *   C = act(z) + residual, computed in FP32 and rounded once to c_dtype.
+ * act is BBS_ACT_NONE, BBS_ACT_SILU or BBS_ACT_GELU.  bias (or NULL) holds N
+ * values of bias_dtype, 16-byte aligned; residual (or NULL) is M x N of c_dtype
+ * with row stride ldr, and may be C itself with ldr == ldc (other overlaps are
+ * not allowed).  C and residual are 16-byte aligned, their row strides >= N and
+ * stride * size % 16 == 0.
+ * z8 (or NULL) receives the 8-bit checkpoint of z for mxfp8_bias_act_bwd: the
+ * MXFP8 copy of the FP32 values, M x N (N % 32 == 0), rounded to nearest even as
+ * the row_mx8 copy of nvfp4_quantize; z must then be finite.
+ * K % 128 == 0 with 8-byte aligned scales is the fast case of large problems.
+ * A may have a decode scale per row.
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for a per-row B scale, for K >= 2^25, or for
+ * an output of 2^24 tiles of 256 x 128 or more. */
+int nvfp4_gemm_bias_act(const bbs_fp4 *A, const bbs_fp4 *B, const void *bias, int32_t bias_dtype,
+                        int32_t act, const void *residual, int64_t ldr, const bbs_mx8 *z8, void *C,
+                        int32_t c_dtype, int64_t ldc, void *stream);
+
+/* Backward pass of act(z) + residual over z's checkpoint:
+ *   dZ = dY * act'(z),   dbias[n] = sum over the rows of dZ[., n],
+ * in FP32 (the sum takes the unrounded dZ), dZ rounded to BF16 and dbias to
+ * dbias_dtype.  (The residual's gradient is dY itself.)  dY is rows x cols of
+ * BF16 patterns with row stride ldy; cols % 16 == 0, % 32 with an activation.
+ * z may be any finite value.  With BBS_ACT_NONE z8 is not read and dZ would be
+ * dY.  dZ (row stride ldz) or dbias may be NULL, and dZ may be dY itself with
+ * ldz == ldy.  dY and dZ are 16-byte aligned with strides that are multiples of
+ * 8.  ws (with dbias): BBS_BIAS_PARTS * cols floats of device workspace, not
+ * kept; calls that overlap in time need one each.  The order of the sums depends
+ * on the sizes and the device's number of CUs alone.
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for 2^31 rows or columns or more. */
+int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t ldy, const bbs_mx8 *z8,
+                       int32_t act, uint16_t *dZ, int64_t ldz, void *dbias, int32_t dbias_dtype,
+                       float *ws, void *stream);
+
+/* nvfp4_gemm_bias_act for a few tokens: y = act(x * W^T + bias) + residual,
+ * operands, sums and errors as nvfp4_gemv.  bias and residual (of y_dtype, row
+ * stride ldr >= N, y itself allowed with ldr == ldy) need no more than their
+ * type's alignment. */
+int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
+                        const void *bias, int32_t bias_dtype, int32_t act, const void *residual,
+                        int64_t ldr, void *y, int32_t y_dtype, int64_t ldy, void *stream);
 
 /* Name of a status code. */
 const char *bbs_strerror(int status);
