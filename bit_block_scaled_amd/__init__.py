@@ -24,6 +24,7 @@ ACT_SILU, ACT_GELU, ACT_NONE = 0, 1, 2
 AMAX_WS_FLOATS = 11264
 GEMV_MAX_TOKENS = 64
 BIAS_PARTS = 64
+MOE_MAX_SLOTS, MOE_MAX_EXPERTS = 32, 1024
 
 
 class Fp4Desc(C.Structure):
@@ -108,7 +109,10 @@ def _load():
                                         C.POINTER(Mx8Desc), vp, i32, i64, vp]
     lib.mxfp8_bias_act_bwd.argtypes = [vp, i64, i64, i64, C.POINTER(Mx8Desc), i32, vp, i64, vp, i32, vp, vp]
     lib.nvfp4_gemv_bias_act.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, i64, vp, i32, i64, vp]
-    for f in ("nvfp4_gemm_bias_act", "mxfp8_bias_act_bwd", "nvfp4_gemv_bias_act", "nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
+    lib.nvfp4_moe_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, vp, vp, i32, vp, i64, vp, vp, i32, i64, vp]
+    lib.nvfp4_moe_ws_bytes.argtypes = [i64, i32, i32, i64]
+    lib.nvfp4_moe_ws_bytes.restype = i64
+    for f in ("nvfp4_moe_gemv", "nvfp4_gemm_bias_act", "mxfp8_bias_act_bwd", "nvfp4_gemv_bias_act", "nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
               "nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_requantize_t", "nvfp4_gemm", "grouped_nvfp4_gemm",
               "s2f6_quantize", "s2f6_combine", "mxfp4_quantize", "nvfp4_gemm_quant",
               "grouped_nvfp4_gemm_quant", "nvfp4_gemm_s2f6", "grouped_nvfp4_gemm_s2f6"):
@@ -558,3 +562,57 @@ def nvfp4_gemv_bias_act(fmt, x, W, y, y_dtype, bias=None, act=ACT_NONE, residual
                                      y.data_ptr(), y_dtype, ldy, s)
     if status:
         _check(status)
+
+
+def moe_workspace(tokens, k, experts, hidden, device="cuda"):
+    """Workspace of an nvfp4_moe_gemv call of these sizes."""
+    n = lib.nvfp4_moe_ws_bytes(tokens, k, experts, hidden)
+    if n < 0:
+        _check(n)
+    return torch.empty((n,), dtype=torch.uint8, device=device)
+
+
+def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=ACT_SILU, residual=None, ws=None,
+                   ldy=None, ldr=None, stream=None):
+    """A whole mixture-of-experts layer for 1 to GEMV_MAX_TOKENS tokens: y[t] =
+    residual[t] + sum over j of weights[t, j] * expert ids[t, j] of x[t], the experts
+    gated (Wg, Wu: stacked [experts * F, K], Wd: [experts * N, F]) or plain (Wg None).
+    x BF16 patterns [T, K]; ids int32 [T, k] (entries outside [0, experts) add
+    nothing), weights float32 [T, k] or None (1); weights in the format fmt (NVFP4
+    with one decode scale an expert); residual [T, N] of y's type, y itself allowed;
+    ws: moe_workspace(...), allocated if None."""
+    if not 1 <= experts <= MOE_MAX_EXPERTS:
+        raise ValueError(f"experts must be in [1, {MOE_MAX_EXPERTS}]")
+    T, cols = x.shape
+    ldx, step = x.stride()
+    K, F, N = Wu.cols, Wd.cols, Wd.rows // experts
+    if cols != K or step != 1 or x.dtype not in _BF16:
+        raise ValueError(f"x must hold rows of {K} BF16 patterns, those of a row adjacent")
+    kind, tensors = _WEIGHTS.get(fmt), [x, ids, y]
+    for w in (Wu, Wd) if Wg is None else (Wu, Wd, Wg):
+        if kind is None or not isinstance(w, kind):
+            raise ValueError("fmt must be FMT_NVFP4 or FMT_MXFP4, and the weights in that format")
+        if kind is NVFP4Tensor and w.s_dec.numel() != experts:
+            raise ValueError("NVFP4 weights need one decode scale an expert")
+        tensors.append(w.codes)
+    if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous int32 tensor of {T} rows")
+    k = ids.shape[1]
+    if weights is not None:
+        if weights.shape != ids.shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+            raise ValueError("weights must be a contiguous float32 tensor of ids' shape")
+        tensors.append(weights)
+    ldy = _output_ld(y, y_dtype, T, N, ldy, "y")
+    if residual is not None:
+        ldr = _output_ld(residual, y_dtype, T, N, ldr, "residual")
+        tensors.append(residual)
+    if T == 1:
+        ldx = K                          # a single row's stride may be anything in PyTorch
+    if ws is None:
+        ws = moe_workspace(T, k, experts, F, x.device)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < lib.nvfp4_moe_ws_bytes(T, k, experts, F):
+        raise ValueError("ws must be a moe_workspace of the call's sizes")
+    s = _on_current(stream, ws, *tensors)
+    _check(lib.nvfp4_moe_gemv(fmt, x.data_ptr(), T, ldx, ids.data_ptr(), _ptr(weights), k, experts,
+                              None if Wg is None else Wg.packed(), Wu.packed(), Wd.packed(), act, _ptr(residual),
+                              ldr or 0, ws.data_ptr(), y.data_ptr(), y_dtype, ldy, s))

@@ -10,7 +10,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libbbs.so")
 SOURCES = ["abi.hip", "quantize.hip", "gemm.hip", "gemm_nvfp4.hip", "gemm_mxfp8.hip",
            "codec.hip", "gated.hip", "gemv.hip",
-           "gemm_nvfp4_gated.hip", "linear.hip", "gemm_nvfp4_linear.hip"]
+           "gemm_nvfp4_gated.hip", "linear.hip", "gemm_nvfp4_linear.hip",
+           "moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -11,6 +11,7 @@
 #include "bbs_kernels.hpp"
 #include "gated.hpp"
 #include "linear.hpp"
+#include "moe.hpp"
 
 static_assert(bbs::kWorkspaceFloats == BBS_AMAX_WS_FLOATS, "workspace size mismatch");
 
@@ -695,6 +696,7 @@ int check_tiles(int64_t M, int64_t N, int64_t TM, int64_t TN) {
 
 bool any_act_ok(int32_t act) { return act_ok(act) || act == BBS_ACT_NONE; }
 static_assert(bbs::kActNone == BBS_ACT_NONE && bbs::kBiasParts == BBS_BIAS_PARTS, "linear layer's constants");
+static_assert(bbs::kMoeSlots == BBS_MOE_MAX_SLOTS && bbs::kMoeExperts == BBS_MOE_MAX_EXPERTS, "expert layer's limits");
 
 // A bias of `cols` values, read `align` bytes at a time (0: value by value).
 int check_bias(const void *b, int32_t dtype, uintptr_t align) {
@@ -957,6 +959,98 @@ int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t l
     p.db_bf16 = dbias_dtype == BBS_OUT_BF16;
     p.part = ws;
     return hip_status(bbs::launch_bias_act_bwd(p, reinterpret_cast<hipStream_t>(stream)), "bias backward launch");
+}
+
+int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden) {
+    g_err[0] = 0;
+    if (tokens < 1 || tokens > BBS_GEMV_MAX_TOKENS || k < 1 || k > BBS_MOE_MAX_SLOTS || experts < 1 ||
+        experts > BBS_MOE_MAX_EXPERTS || hidden < 1 || hidden >= (int64_t)1 << 24)
+        return fail(BBS_EINVAL, "tokens, k, experts or hidden out of range");
+    return bbs::moe_ws_bytes(tokens, k, experts, hidden);
+}
+
+int nvfp4_moe_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const int32_t *ids,
+                   const float *weights, int32_t k, int32_t experts, const void *Wg, const void *Wu, const void *Wd,
+                   int32_t act, const void *residual, int64_t ldr, void *ws, void *y, int32_t y_dtype, int64_t ldy,
+                   void *stream) {
+    g_err[0] = 0;
+    int st;
+    if (!x) return fail(BBS_EINVAL, "null x");
+    if (!y) return fail(BBS_EINVAL, "null y");
+    if (!ids) return fail(BBS_EINVAL, "null ids");
+    if (!ws || !aligned(ws, 16)) return fail(BBS_EINVAL, "null or misaligned workspace");
+    if (!dtype_ok(y_dtype)) return fail(BBS_EINVAL, "bad y_dtype");
+    if (!any_act_ok(act)) return fail(BBS_EINVAL, "bad act");
+    if (Wg && act == BBS_ACT_NONE) return fail(BBS_EINVAL, "gated experts need an activation");
+    if (tokens < 1 || tokens > BBS_GEMV_MAX_TOKENS)
+        return fail(BBS_EINVAL, "tokens must be in [1, %d]", BBS_GEMV_MAX_TOKENS);
+    if (k < 1 || k > BBS_MOE_MAX_SLOTS) return fail(BBS_EINVAL, "k must be in [1, %d]", BBS_MOE_MAX_SLOTS);
+    if (experts < 1 || experts > BBS_MOE_MAX_EXPERTS)
+        return fail(BBS_EINVAL, "experts must be in [1, %d]", BBS_MOE_MAX_EXPERTS);
+    bbs::MoeParams p{};
+    const void *const w[3] = {Wg, Wu, Wd};
+    const char *const name[3] = {"Wg", "Wu", "Wd"};
+    bbs::GemvParams::Weight *const to[3] = {&p.g, &p.u, &p.d};
+    int64_t rows[3], cols[3];
+    int tile2d[3];
+    for (int i = Wg ? 0 : 1; i < 3; ++i) {
+        if (fmt == BBS_FMT_NVFP4) {
+            const bbs_fp4 *d = static_cast<const bbs_fp4 *>(w[i]);
+            if ((st = check_fp4(d, name[i], true))) return st;
+            if (d->sdec_per_row) return fail(BBS_ENOTSUP, "weights with a per-row decode scale");
+            *to[i] = {d->codes, d->scales, d->s_dec};
+            rows[i] = d->rows;
+            cols[i] = d->cols;
+            tile2d[i] = d->tile2d;
+        } else if (fmt == BBS_FMT_MXFP4) {
+            const bbs_mx4 *d = static_cast<const bbs_mx4 *>(w[i]);
+            if ((st = check_mx4(d, name[i]))) return st;
+            *to[i] = {d->codes, d->scales, nullptr};
+            rows[i] = d->rows;
+            cols[i] = d->cols;
+            tile2d[i] = 0;
+        } else {
+            return fail(BBS_EINVAL, "fmt must be BBS_FMT_NVFP4 or BBS_FMT_MXFP4");
+        }
+        const int64_t each = rows[i] / experts;
+        if (rows[i] % experts || (fmt == BBS_FMT_NVFP4 && each % 16))
+            return fail(BBS_EINVAL, "%s must hold the same number of rows for every expert (NVFP4: a multiple of 16)",
+                        name[i]);
+    }
+    if (Wg && (rows[0] != rows[1] || cols[0] != cols[1])) return fail(BBS_EINVAL, "Wg and Wu must have the same shape");
+    if ((Wg && tile2d[0] != tile2d[1]) || tile2d[2] != tile2d[1])
+        return fail(BBS_ENOTSUP, "weights with different tile2d");
+    p.K = cols[1];
+    p.F = rows[1] / experts;
+    p.N = rows[2] / experts;
+    if (cols[2] != p.F) return fail(BBS_EINVAL, "Wd.cols must equal an expert's hidden rows");
+    // row offsets inside a workgroup are 32 bits wide, a launch holds fewer than 2^32 threads a dimension
+    const int64_t lim = (int64_t)1 << 24;
+    if (p.K >= lim || p.F >= lim || p.N >= lim) return fail(BBS_ENOTSUP, "2^24 features or more");
+    if (ldx < p.K || ldx % 8) return fail(BBS_EINVAL, "ldx must be >= K and a multiple of 8");
+    if (!aligned(x, 16)) return fail(BBS_EINVAL, "x not 16-byte aligned");
+    if (!aligned(ids, 4) || !aligned(weights, 4)) return fail(BBS_EINVAL, "ids and weights must be 4-byte aligned");
+    const uintptr_t es = y_dtype == BBS_OUT_BF16 ? 2 : 4;
+    if (ldy < p.N || !aligned(y, es)) return fail(BBS_EINVAL, "y must be aligned to its type, with a row stride >= N");
+    if (residual && (ldr < p.N || !aligned(residual, es)))
+        return fail(BBS_EINVAL, "residual must be aligned to its type, with a row stride >= N");
+    p.x = x;
+    p.T = tokens;
+    p.ldx = ldx;
+    p.ids = ids;
+    p.weights = weights;
+    p.k = k;
+    p.E = experts;
+    p.tile2d = tile2d[1];
+    p.gated = Wg != nullptr;
+    p.act = act;
+    p.r = residual;
+    p.ldr = ldr;
+    p.y = y;
+    p.ldy = ldy;
+    p.bf16_out = y_dtype == BBS_OUT_BF16;
+    p.ws = static_cast<uint8_t *>(ws);
+    return hip_status(bbs::launch_moe(p, fmt == BBS_FMT_MXFP4, reinterpret_cast<hipStream_t>(stream)), "moe launch");
 }
 
 }  // extern "C"

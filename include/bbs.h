@@ -54,6 +54,10 @@ enum bbs_act { BBS_ACT_SILU = 0, BBS_ACT_GELU = 1, BBS_ACT_NONE = 2 };
 /* Most tokens nvfp4_gemv and nvfp4_gated_gemv take in one call. */
 #define BBS_GEMV_MAX_TOKENS 64
 
+/* Most experts a token may choose in nvfp4_moe_gemv, and most experts there may be. */
+#define BBS_MOE_MAX_SLOTS 32
+#define BBS_MOE_MAX_EXPERTS 1024
+
 /* mxfp8_bias_act_bwd needs up to this many floats of device workspace a column. */
 #define BBS_BIAS_PARTS 64
 
@@ -442,6 +446,36 @@ int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t l
 int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const void *W,
                         const void *bias, int32_t bias_dtype, int32_t act, const void *residual,
                         int64_t ldr, void *y, int32_t y_dtype, int64_t ldy, void *stream);
+
+/* A whole mixture-of-experts layer for 1 to BBS_GEMV_MAX_TOKENS tokens, in two
+ * kernels:
+ *   y[t] = residual[t] + sum over j < k of weights[t, j] * expert_e(x[t]),  e = ids[t, j],
+ *   expert_e(x) = (act(x * Wg_e^T) * (x * Wu_e^T)) * Wd_e^T,   gated (Wg given), or
+ *   expert_e(x) = act(x * Wu_e^T) * Wd_e^T                     plain (Wg NULL).
+ * fmt, x and the weights' formats as nvfp4_gemv.  Wg and Wu stack the experts'
+ * F x K matrices (experts * F rows), Wd their N x F ones, all with the same
+ * scale layout; NVFP4 weights have one decode scale an expert (s_dec[e]) and F and N
+ * that are multiples of 16.  ids is tokens x k: an entry below 0 or >= experts is a
+ * dropped slot and adds nothing (a token without experts gets its residual, or
+ * +0); an expert chosen twice by a token counts twice.  weights is tokens x k FP32, or
+ * NULL (1).  act is SiLU or GELU, for plain experts also BBS_ACT_NONE.
+ * residual (or NULL) is tokens x N of y_dtype with row stride ldr, and may be y.
+ * Everything is computed in FP32 and rounded once to y_dtype, except that the
+ * hidden values are held in two BF16 parts (16 significant bits) for BF16 outputs
+ * and in three (24) for FP32 ones; they must be below 2^127.  The sums' order
+ * depends on sizes, format and routing alone; a token's answer then differs from
+ * what it gets beside other tokens by the rounding of FP32 sums.
+ * ws: nvfp4_moe_ws_bytes(tokens, k, experts, F) bytes of device workspace, 16-byte
+ * aligned, not kept; calls that overlap in time need one each.
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale or with
+ * different tile2d, or for 2^24 features or more. */
+int nvfp4_moe_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const int32_t *ids,
+                   const float *weights, int32_t k, int32_t experts, const void *Wg, const void *Wu,
+                   const void *Wd, int32_t act, const void *residual, int64_t ldr, void *ws, void *y,
+                   int32_t y_dtype, int64_t ldy, void *stream);
+
+/* Bytes of workspace of such a call (negative: BBS_EINVAL). */
+int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden);
 
 /* Name of a status code. */
 const char *bbs_strerror(int status);
