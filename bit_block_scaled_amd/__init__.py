@@ -110,7 +110,7 @@ def _load():
     lib.mxfp8_bias_act_bwd.argtypes = [vp, i64, i64, i64, C.POINTER(Mx8Desc), i32, vp, i64, vp, i32, vp, vp]
     lib.nvfp4_gemv_bias_act.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, i64, vp, i32, i64, vp]
     lib.nvfp4_moe_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, vp, vp, i32, vp, i64, vp, vp, i32, i64, vp]
-    lib.nvfp4_moe_ws_bytes.argtypes = [i64, i32, i32, i64]
+    lib.nvfp4_moe_ws_bytes.argtypes = [i64, i32, i32, i64, i64]
     lib.nvfp4_moe_ws_bytes.restype = i64
     for f in ("nvfp4_moe_gemv", "nvfp4_gemm_bias_act", "mxfp8_bias_act_bwd", "nvfp4_gemv_bias_act", "nvfp4_gated_gemm", "mxfp8_gemm_gated_bwd", "nvfp4_gemv", "nvfp4_gated_gemv",
               "nvfp4_quantize", "nvfp4_quantize_noalloc", "mxfp8_requantize_t", "nvfp4_gemm", "grouped_nvfp4_gemm",
@@ -564,9 +564,9 @@ def nvfp4_gemv_bias_act(fmt, x, W, y, y_dtype, bias=None, act=ACT_NONE, residual
         _check(status)
 
 
-def moe_workspace(tokens, k, experts, hidden, device="cuda"):
+def moe_workspace(tokens, k, experts, hidden, features, device="cuda"):
     """Workspace of an nvfp4_moe_gemv call of these sizes."""
-    n = lib.nvfp4_moe_ws_bytes(tokens, k, experts, hidden)
+    n = lib.nvfp4_moe_ws_bytes(tokens, k, experts, hidden, features)
     if n < 0:
         _check(n)
     return torch.empty((n,), dtype=torch.uint8, device=device)
@@ -609,8 +609,8 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
     if T == 1:
         ldx = K                          # a single row's stride may be anything in PyTorch
     if ws is None:
-        ws = moe_workspace(T, k, experts, F, x.device)
-    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < lib.nvfp4_moe_ws_bytes(T, k, experts, F):
+        ws = moe_workspace(T, k, experts, F, N, x.device)
+    elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < lib.nvfp4_moe_ws_bytes(T, k, experts, F, N):
         raise ValueError("ws must be a moe_workspace of the call's sizes")
     s = _on_current(stream, ws, *tensors)
     _check(lib.nvfp4_moe_gemv(fmt, x.data_ptr(), T, ldx, ids.data_ptr(), _ptr(weights), k, experts,

@@ -961,12 +961,13 @@ int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t l
     return hip_status(bbs::launch_bias_act_bwd(p, reinterpret_cast<hipStream_t>(stream)), "bias backward launch");
 }
 
-int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden) {
+int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden, int64_t features) {
     g_err[0] = 0;
     if (tokens < 1 || tokens > BBS_GEMV_MAX_TOKENS || k < 1 || k > BBS_MOE_MAX_SLOTS || experts < 1 ||
-        experts > BBS_MOE_MAX_EXPERTS || hidden < 1 || hidden >= (int64_t)1 << 24)
-        return fail(BBS_EINVAL, "tokens, k, experts or hidden out of range");
-    return bbs::moe_ws_bytes(tokens, k, experts, hidden);
+        experts > BBS_MOE_MAX_EXPERTS || hidden < 1 || hidden >= (int64_t)1 << 24 || features < 1 ||
+        features >= (int64_t)1 << 24)
+        return fail(BBS_EINVAL, "tokens, k, experts, hidden or features out of range");
+    return bbs::moe_ws_bytes(tokens, k, experts, hidden, features);
 }
 
 int nvfp4_moe_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, const int32_t *ids,
@@ -1050,6 +1051,7 @@ int nvfp4_moe_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, 
     p.ldy = ldy;
     p.bf16_out = y_dtype == BBS_OUT_BF16;
     p.ws = static_cast<uint8_t *>(ws);
+    p.part = reinterpret_cast<float *>(p.ws + bbs::moe_hidden_bytes(tokens, k, p.F));
     return hip_status(bbs::launch_moe(p, fmt == BBS_FMT_MXFP4, reinterpret_cast<hipStream_t>(stream)), "moe launch");
 }
 

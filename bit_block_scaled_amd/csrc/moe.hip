@@ -1,14 +1,24 @@
 // A whole mixture-of-experts layer for a few tokens with 4-bit weights (gfx950):
 //   y[t] = r[t] + sum_j w[t, j] (act(x[t] Wg_e^T) * (x[t] Wu_e^T)) Wd_e^T,   e = ids[t, j]
-// or, for plain experts, act(x[t] Wu_e^T) Wd_e^T, in two kernels.
+// or, for plain experts, act(x[t] Wu_e^T) Wd_e^T.
 //
 // The chosen experts' weights bound the layer: each is read once, against 2 flops
-// a weight and token.  The first kernel's workgroups take one expert and a few of
-// its hidden rows; they find the expert's tokens themselves by looking through
-// the ids (T k of them), so nothing has to be sorted first.  The second kernel's
-// workgroups take a few output columns of all the chosen experts: an output's
-// sum over the experts then stays in one workgroup, in a fixed order, without
-// atomics.  Its waves share the steps of all experts evenly, whatever the routing.
+// a weight and token.  Three forms, by the launch rules at the end:
+//   - up to four tokens, two kernels with 4 x 4 x 4 products.  The first kernel's
+//     workgroups take one expert and a few of its hidden rows; they find the expert's
+//     tokens themselves by looking through the ids (T k of them), so nothing has to be
+//     sorted first.  The second kernel's workgroups take a few output columns of all
+//     the chosen experts: an output's sum over the experts then stays in one
+//     workgroup, in a fixed order, without atomics.  Its waves share the steps of all
+//     experts evenly, whatever the routing.
+//   - more tokens: the same two with 16 x 16 x 32 products.
+//   - more tokens and large weights: one workgroup a CU streams its even share of all
+//     the experts' weights through registers, a kernel for each projection, and a
+//     third kernel adds up the experts' outputs.
+// Measured, replayed from a graph (codes and scales at TB/s in brackets): 1 token,
+// 8 of 64 plain experts, 50 MB: 17.7 us (2.9); 1 token, 2 of 8 gated, 177 MB: 45.9 us
+// (3.9); 16 tokens, MXFP4, 430 MB: 112 us (3.8); 64 tokens, 8 of 64, NVFP4, 61 experts
+// chosen, 582 MB: 184 us (3.2).
 //
 // The hidden values go between the kernels as two BF16 parts (three for FP32
 // outputs): h = hi + lo to 2^-16, below the output's rounding.  A part is one
@@ -37,10 +47,10 @@ struct MoePlan {
 __device__ __forceinline__ MoePlan plan_of(const MoeParams &p) {
     const int64_t pairs = p.T * p.k, slots = pairs < p.E ? pairs : p.E;
     MoePlan m;
-    m.expert = reinterpret_cast<int32_t *>(p.ws);
+    m.h = reinterpret_cast<uint16_t *>(p.ws);
+    m.entry = reinterpret_cast<MoeEntry *>(m.h + 3 * pairs * p.F);
+    m.expert = reinterpret_cast<int32_t *>(m.entry + slots * p.T);
     m.count = m.expert + slots;
-    m.entry = reinterpret_cast<MoeEntry *>(m.count + slots);
-    m.h = reinterpret_cast<uint16_t *>(p.ws + (slots * (8 + p.T * (int64_t)sizeof(MoeEntry)) + 15) / 16 * 16);
     return m;
 }
 
@@ -51,23 +61,31 @@ struct Routed {
 };
 
 // Every wave gets here; `keep` (the same for the workgroup): the slot's plan is
-// written for the second kernel.
+// written for the second kernel.  The ids are loaded eight at a time, all before
+// the first is looked at (one after the other they took longer than the weights
+// of a small expert).
 __device__ __forceinline__ void route(Routed &rt, const MoeParams &p, int slot, bool keep) {
     if (threadIdx.x < 64) {
         const int t = threadIdx.x;
         const bool by_pair = p.T * p.k < p.E;
         const int e = by_pair ? p.ids[slot] : slot;
+        const int row = min(t, (int)p.T - 1) * p.k;
         int first = -1;
         float w = 0.0f;
-        if (t < p.T && e >= 0 && e < p.E) {
-            for (int j = 0; j < p.k; ++j) {
-                const int at = t * p.k + j;
-                if (p.ids[at] != e) continue;
-                if (first < 0) first = at;
-                if (keep) w += p.weights ? p.weights[at] : 1.0f;      // an expert chosen twice counts twice
+        for (int j0 = 0; j0 < p.k; j0 += 8) {
+            int id[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) id[j] = p.ids[row + min(j0 + j, p.k - 1)];
+#pragma unroll
+            for (int j = 7; j >= 0; --j)
+                if (id[j] == e && j0 + j < p.k && (first < 0 || first >= row + j0)) first = row + j0 + j;
+            if (keep) {                                               // an expert chosen twice counts twice
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (id[j] == e && j0 + j < p.k) w += p.weights ? p.weights[row + j0 + j] : 1.0f;
             }
         }
-        uint64_t mask = __ballot(first >= 0);
+        uint64_t mask = __ballot(first >= 0 && t < p.T && e >= 0 && e < p.E);
         if (by_pair && mask && __shfl(first, __builtin_ctzll(mask), 64) != slot) mask = 0;
         const int count = __builtin_popcountll(mask);
         const int rank = __builtin_popcountll(mask & ((1ull << t) - 1));
@@ -112,13 +130,13 @@ __device__ __forceinline__ GemvParams up_product(const MoeParams &p, int e) {
 
 // Hidden value n of a pair from its sums, as its parts.
 template <int SC, int NM>
-__device__ __forceinline__ void finish_hidden(const MoeParams &p, const GemvParams &q, const MoePlan &m, int pair,
+__device__ __forceinline__ void finish_hidden(const MoeParams &p, const GemvParams &q, uint16_t *hidden, int pair,
                                               int64_t n, const float (&v)[2]) {
     float h = SC == kRows32 ? v[0] : v[0] * q.w.s_dec[0];
     if (p.act == kActSilu) h = gate_act<kActSilu, false>(h);
     else if (p.act == kActGelu) h = gate_act<kActGelu, false>(h);
     if (NM == 2) h *= SC == kRows32 ? v[1] : v[1] * q.u.s_dec[0];
-    uint16_t *at = m.h + pair * p.F + n;
+    uint16_t *at = hidden + pair * p.F + n;
     const int64_t part = p.T * p.k * p.F;
     const int parts = p.bf16_out ? 2 : 3;
     for (int i = 0; i < parts; ++i) {
@@ -129,15 +147,18 @@ __device__ __forceinline__ void finish_hidden(const MoeParams &p, const GemvPara
     }
 }
 
-constexpr int kMoeSplit = 8;     // waves of a workgroup
+constexpr int kSplit = 8;              // waves of a workgroup
+// Of moe_up_few_kernel, whose workgroups are many (hidden rows x experts): 2 of 8
+// experts, 1 token, 30.1 us against 32.5 with four and 35 with eight.
+constexpr int kUpFewSplit = 2;
 
 // ---------------------------------------------------------------------------
 // Up projections, up to four tokens at a time (4 x 4 x 4 products).
 // ---------------------------------------------------------------------------
 template <int SC, int NM, int TT, int R>
-__global__ __launch_bounds__(64 * kMoeSplit) void moe_up_few_kernel(MoeParams p) {
+__global__ __launch_bounds__(64 * kUpFewSplit) void moe_up_few_kernel(MoeParams p) {
     constexpr int NO = TT * R * 4;                       // outputs, of NM sums each
-    __shared__ float part[kMoeSplit][NM * NO];
+    __shared__ float part[kUpFewSplit][NM * NO];
     __shared__ Routed rt;
     route(rt, p, blockIdx.y, blockIdx.x == 0);
     const int count = rt.count;
@@ -189,7 +210,7 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_up_few_kernel(MoeParams p)
                 for (int w = 0; w < NM; ++w) v[w] += part[k][w * NO + o];
             const int i = c + o / (R * 4);
             const int64_t n = n0 + o % (R * 4);
-            if (i < count && n < p.F) finish_hidden<SC, NM>(p, q, m, rt.pair[i], n, v);
+            if (i < count && n < p.F) finish_hidden<SC, NM>(p, q, m.h, rt.pair[i], n, v);
         }
         __syncthreads();
     }
@@ -200,10 +221,10 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_up_few_kernel(MoeParams p)
 // through LDS as in the matrix-vector products).
 // ---------------------------------------------------------------------------
 template <int SC, int NM, int NR>
-__global__ __launch_bounds__(64 * kMoeSplit) void moe_up_tile_kernel(MoeParams p) {
+__global__ __launch_bounds__(64 * kSplit) void moe_up_tile_kernel(MoeParams p) {
     constexpr int NO = NR * 256;                          // sums of one matrix
     constexpr int kWave = NM * NO * 4 > 4096 ? NM * NO * 4 : 4096;
-    __shared__ __align__(16) uint8_t lds[kMoeSplit * kWave];
+    __shared__ __align__(16) uint8_t lds[kSplit * kWave];
     __shared__ Routed rt;
     route(rt, p, blockIdx.y, blockIdx.x == 0);
     const int count = rt.count;
@@ -276,10 +297,484 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_up_tile_kernel(MoeParams p
             // consecutive o: rows 4 g + v of one token
             const int l = (o >> 2) & 63, t = c + (l & 15);
             const int64_t n = n0 + (o >> 8) * 16 + (l >> 4) * 4 + (o & 3);
-            if (t < count && n < p.F) finish_hidden<SC, NM>(p, q, m, rt.pair[t], n, v);
+            if (t < count && n < p.F) finish_hidden<SC, NM>(p, q, m.h, rt.pair[t], n, v);
         }
         __syncthreads();
     }
+}
+
+// Four consecutive hidden values of a pair; sv, su: the decode scales.
+template <int NM>
+__device__ __forceinline__ void finish_hidden4(const MoeParams &p, uint16_t *hidden, int pair, int64_t n, const f32x4 &v,
+                                               const f32x4 &u, float sv, float su) {
+    float h[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        h[q] = v[q] * sv;
+        if (p.act == kActSilu) h[q] = gate_act<kActSilu, false>(h[q]);
+        else if (p.act == kActGelu) h[q] = gate_act<kActGelu, false>(h[q]);
+        if (NM == 2) h[q] *= u[q] * su;
+    }
+    uint16_t *at = hidden + pair * p.F + n;
+    const int parts = p.bf16_out ? 2 : 3;
+    for (int i = 0; i < parts; ++i, at += p.T * p.k * p.F) {
+        const uint2 b = make_uint2(pk_bf16(h[0], h[1]), pk_bf16(h[2], h[3]));
+        *reinterpret_cast<uint2 *>(at) = b;
+        const uint32_t w[4] = {b.x << 16, b.x & 0xFFFF0000u, b.y << 16, b.y & 0xFFFF0000u};
+        // an infinite part leaves nothing over (not infinity less infinity)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            h[q] = (w[q] & 0x7FFFFFFFu) == 0x7F800000u ? 0.0f : h[q] - __uint_as_float(w[q]);
+    }
+}
+
+__device__ __forceinline__ void finish_output(const MoeParams &p, int64_t t, int64_t n, float v) {
+    if (p.r) v += value_at(p.r, t * p.ldr + n, p.bf16_out);
+    if (p.bf16_out) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(v, v);
+    else static_cast<float *>(p.y)[t * p.ldy + n] = v;
+}
+
+// ---------------------------------------------------------------------------
+// Streaming kernels: 16 x 16 x 32 products, sixteen tokens (or rows of parts of hidden
+// values) by sixteen weight rows, 512 K values a step.
+//
+// One workgroup of eight waves a CU, two a SIMD, with 256 registers each for the
+// weights in flight (four a SIMD with half of them measured the same, and the rows
+// in LDS leave no room for them in the up projection).  Each workgroup lists the units
+// first: an expert and up to a tile's rows of its tokens, in ascending order.
+//
+// Bound, at 64 tokens, by the expansion of the codes: two vector instructions a code
+// and half of one for the exchange of lanes (counters: vector units 70% busy, L1, LDS
+// and the matrix units below 25%); MXFP4 codes, half an instruction each, by the loads.
+// ---------------------------------------------------------------------------
+struct Units {
+    uint64_t *mask;                    // the tokens of each expert
+    int32_t *first;                    // its first entry
+    int32_t *ids, *entry;              // of each pair; entry: pair | token << 16
+    float *weight;                     // of each entry
+    int32_t *unit;                     // expert | first entry << 10 | entries << 21
+    int32_t *count;                    // the units
+};
+
+__device__ __forceinline__ Units units_at(uint8_t *lds, const MoeParams &p) {
+    const int pairs = (int)p.T * p.k;
+    Units u;
+    u.mask = reinterpret_cast<uint64_t *>(lds);
+    u.first = reinterpret_cast<int32_t *>(u.mask + p.E);
+    u.ids = u.first + p.E;
+    u.entry = u.ids + pairs;
+    u.weight = reinterpret_cast<float *>(u.entry + pairs);
+    u.unit = reinterpret_cast<int32_t *>(u.weight + pairs);
+    u.count = u.unit + pairs;
+    return u;
+}
+
+__device__ __forceinline__ void list_units(const Units &u, const MoeParams &p, int tok) {
+    const int pairs = (int)p.T * p.k, n = blockDim.x;
+    for (int e = threadIdx.x; e < p.E; e += n) u.mask[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += n) {
+        const int e = p.ids[i];
+        u.ids[i] = e;
+        if (e >= 0 && e < p.E) atomicOr(reinterpret_cast<unsigned long long *>(u.mask + e), 1ull << (i / p.k));
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        int entries = 0, units = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 64) {
+            const int e = e0 + threadIdx.x;
+            const int c = e < p.E ? __builtin_popcountll(u.mask[e]) : 0;
+            // inclusive sums over the lanes: entries low, units high
+            const int n_units = (c + tok - 1) / tok;
+            int sum = c | n_units << 16;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(sum, o, 64);
+                if ((int)threadIdx.x >= o) sum += v;
+            }
+            const int first = entries + (sum & 0xFFFF) - c;
+            int at = units + (sum >> 16) - n_units;
+            if (e < p.E) u.first[e] = first;
+            for (int i = 0; i < c; i += tok) u.unit[at++] = e | (first + i) << 10 | min(tok, c - i) << 21;
+            const int all = __shfl(sum, 63, 64);
+            entries += all & 0xFFFF;
+            units += all >> 16;
+        }
+        if (threadIdx.x == 0) *u.count = units;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += n) {
+        const int e = u.ids[i], t = i / p.k, end = t * p.k + p.k;
+        bool again = e < 0 || e >= p.E;
+        for (int j = t * p.k; j < i; ++j) again |= u.ids[j] == e;
+        if (again) continue;
+        float w = p.weights ? p.weights[i] : 1.0f;
+        for (int j = i + 1; j < end; ++j)                 // an expert chosen twice counts twice
+            if (u.ids[j] == e) w += p.weights ? p.weights[j] : 1.0f;
+        const int at = u.first[e] + __builtin_popcountll(u.mask[e] & ((1ull << t) - 1));
+        u.entry[at] = i | t << 16;
+        u.weight[at] = w;
+    }
+    __syncthreads();
+}
+
+// The weights of a step, 512 K values of NM NR tiles of 16 rows, in registers.  Lane
+// 16 g + i multiplies row i at K values 128 g .. + 128 of the step: 64 bytes of
+// codes.  They are loaded so that four lanes in a row (a quad) take 64 bytes in a
+// row, each of its four rows with one load, and change lanes in registers: with each
+// lane loading its own row, every 16 bytes were an access of their own in L1, one a
+// cycle, and bound the kernel.
+template <int NM, int NR>
+struct TileStep {
+    uint4 c[NM][NR][4];                // 16 bytes m: of the quad's row m
+    uint2 s[NM][NR];                   // the lane's eight E4M3 bytes, or four E8M0 ones in x
+};
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t quad_perm(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, false);
+}
+
+// Lanes q and q ^ 1 (CTRL 0xB1, bit: q & 1) or q ^ 2 (0x4E, q & 2) swap b of the lower
+// one with a of the upper one.
+template <int CTRL>
+__device__ __forceinline__ void quad_swap(uint32_t &a, uint32_t &b, bool upper) {
+    const uint32_t t = quad_perm<CTRL>(upper ? a : b);
+    a = upper ? t : a;
+    b = upper ? b : t;
+}
+
+// From 16 bytes q of rows 0 .. 3 to 16 bytes 0 .. 3 of row q, q being the lane's place
+// in its quad.
+__device__ __forceinline__ void quad_transpose(uint4 (&v)[4]) {
+    const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+    for (int m = 0; m < 4; m += 2) {
+        quad_swap<0xB1>(v[m].x, v[m + 1].x, odd);
+        quad_swap<0xB1>(v[m].y, v[m + 1].y, odd);
+        quad_swap<0xB1>(v[m].z, v[m + 1].z, odd);
+        quad_swap<0xB1>(v[m].w, v[m + 1].w, odd);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        quad_swap<0x4E>(v[m].x, v[m + 2].x, high);
+        quad_swap<0x4E>(v[m].y, v[m + 2].y, high);
+        quad_swap<0x4E>(v[m].z, v[m + 2].z, high);
+        quad_swap<0x4E>(v[m].w, v[m + 2].w, high);
+    }
+}
+
+// Where a wave loads weights from: the matrices at the tile's first row, and from
+// there the lane's place in the quad's first row and its own row's scales.
+template <int NM, int NR>
+struct TileSource {
+    const uint8_t *codes[NM], *scales[NM];
+    uint32_t code, pitch, scale[NR];
+};
+
+// k0: K value of the step.
+template <int SC, int NM, int NR>
+__device__ __forceinline__ void load_tile(TileStep<NM, NR> &st, const TileSource<NM, NR> &t, int64_t k0) {
+#pragma unroll
+    for (int w = 0; w < NM; ++w)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                st.c[w][r][m] = *reinterpret_cast<const uint4 *>(t.codes[w] + k0 / 2 + (t.code + (16 * r + m) * t.pitch));
+            if (SC == kRows32) __builtin_memcpy(&st.s[w][r].x, t.scales[w] + k0 / 32 + t.scale[r], 4);
+            else __builtin_memcpy(&st.s[w][r], t.scales[w] + k0 / 16 + t.scale[r], 8);
+        }
+}
+
+// x: the step's rows in LDS, 1024 bytes each, NT tiles of 16; row: the lane's in a tile.
+template <int SC, int NM, int NR, int NT>
+__device__ __forceinline__ void add_tile(f32x4 (&acc)[NM][NR][NT], TileStep<NM, NR> &st, const uint8_t *x, int row) {
+    const int g = (threadIdx.x & 63) >> 4;
+    uint4 xv[2][4][NT];
+    // the rows' 64 bytes m are read while those before them are multiplied
+    auto read = [&](int m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                xv[m & 1][j][t] = *reinterpret_cast<const uint4 *>(x + (16 * t + row) * 1024 + 256 * g +
+                                                                   16 * ((4 * m + j) ^ row));
+    };
+    read(0);
+#pragma unroll
+    for (int w = 0; w < NM; ++w)
+#pragma unroll
+        for (int r = 0; r < NR; ++r) quad_transpose(st.c[w][r]);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+        if (m < 3) read(m + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        f32x2 sc[NM][NR];                                 // of blocks 2 m and 2 m + 1 (MXFP4: m)
+#pragma unroll
+        for (int w = 0; w < NM; ++w)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const uint2 b = st.s[w][r];
+                if (SC == kRows32) sc[w][r][0] = sc[w][r][1] = e8m0_value(b.x >> (8 * m) & 0xFFu);
+                else if (m & 1) sc[w][r] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)(m < 2 ? b.x : b.y), 1.0f, true);
+                else sc[w][r] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8((int)(m < 2 ? b.x : b.y), 1.0f, false);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int w = 0; w < NM; ++w)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const bf16x8 c = expand8<SC>(word(st.c[w][r][m], j), sc[w][r][j >> 1]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        acc[w][r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            c, __builtin_bit_cast(bf16x8, xv[m & 1][j][t]), acc[w][r][t], 0, 0, 0);
+                }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// n steps through a ring of D in registers: issue(step) loads the next one (past
+// the last it loads what is there again), use(step) multiplies the oldest; begun()
+// comes between the first loads and the first use.  No load depends on a branch:
+// the compiler then waits for a step's own loads and not for those behind them.
+template <int D, typename Step, typename Issue, typename Begun, typename Use>
+__device__ __forceinline__ void run_ring(int64_t n, Issue issue, Begun begun, Use use) {
+    Step ring[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) issue(ring[d]);
+    begun();
+    for (int64_t i = D; i <= n; i += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            use(ring[d]);
+            issue(ring[d]);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < n % D) use(ring[d]);
+}
+
+__device__ __forceinline__ float scalar(float v) {
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
+// NP = 0: up projection, x rows to hidden values.  Else: down projection, NP parts of
+// hidden values to a pair's outputs (weighted), of each range of K.
+//
+// A workgroup takes an even share of the tiles (16 NR weight rows of a range of a
+// unit), unit by unit.  The unit's rows lie in LDS, and its tiles' steps, one tile's
+// after another's, are cut into even parts for the waves.  A wave that comes into a
+// tile behind its first step leaves its sums in LDS for the one that began it.
+template <int SC, int NM, int NR, int NP, int NT, int D>
+__global__ __launch_bounds__(64 * kMoeTileWaves, 2) void moe_stream_kernel(MoeParams p, MoeShape sh) {
+    static_assert(NM * NR == 2, "a tile's sums fill a wave's buffer");
+    constexpr int NW = kMoeTileWaves;
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int64_t K = NP ? p.F : p.K, rows = NP ? p.N : p.F;
+    const int64_t most = moe_rows_bytes(sh);
+    uint8_t *const xs = lds;                                                   // [step][row][1024 bytes]
+    float *const part = reinterpret_cast<float *>(lds + most);
+    const Units un = units_at(lds + most + moe_sums_bytes(NT), p);
+    const int tok = NP ? sh.rows / 16 * (16 / (NP ? NP : 1)) : sh.rows;
+    list_units(un, p, tok);
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = i & (sh.rows - 1);        // (rows: 4, 8, or 16 a tile)
+    const int64_t blocks = (rows + 16 * NR - 1) / (16 * NR), tiles = *un.count * sh.ranges * blocks;
+    int64_t at = tiles * blockIdx.x / gridDim.x;
+    const int64_t last = tiles * (blockIdx.x + 1) / gridDim.x;
+    uint16_t *const h = reinterpret_cast<uint16_t *>(p.ws);
+    const int64_t pairs = p.T * p.k;
+
+    while (at < last) {
+        // blocks b0 .. b1 of one range of one unit
+        const int64_t ur = at / blocks, b0 = at - ur * blocks, b1 = min(blocks, b0 + last - at);
+        at += b1 - b0;
+        const int u = (int)(ur / sh.ranges), range = (int)(ur - (int64_t)u * sh.ranges);
+        const int unit = __builtin_amdgcn_readfirstlane(un.unit[u]), e = unit & 1023, n = unit >> 21;
+        const int *const entry = un.entry + (unit >> 10 & 2047);
+        const int64_t klo = range * sh.range, khi = min(K, klo + sh.range);
+        const int steps = (int)((khi - klo + kMoeStep - 1) / kMoeStep);
+        const int64_t all = (b1 - b0) * steps, s0 = all * wave / NW, s1 = all * (wave + 1) / NW;
+        // the decode scales, loaded here: a load's wait among the steps would be one for
+        // all the weights before it
+        float sv = 1.0f, su = 1.0f;
+        if (SC != kRows32) {
+            sv = scalar((NP ? p.d : NM == 2 ? p.g : p.u).s_dec[e]);
+            if (NM == 2) su = scalar(p.u.s_dec[e]);
+        }
+        // a last step that K ends in starts earlier, at K - 512; in LDS its rows are zero
+        // where the step before has had them
+        auto step_k = [&](int s) { return min(klo + s * kMoeStep, K - kMoeStep); };
+        // a block at the end of the rows starts earlier, and leaves out the rows that the
+        // block before it has: their sums are cut elsewhere there
+        auto first_row = [&](int64_t blk) { return min(blk * (16 * NR), rows - 16 * NR); };
+        GemvParams::Weight mat[NM];
+        mat[0] = expert_of(NP ? p.d : NM == 2 ? p.g : p.u, e, rows, K, SC);
+        if (NM == 2) mat[NM - 1] = expert_of(p.u, e, rows, K, SC);
+        TileSource<NM, NR> src;
+        src.pitch = (uint32_t)(K / 2);
+        src.code = (lane >> 2 & 3) * 4 * src.pitch + 64 * g + 16 * (lane & 3);
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+            src.scale[r] = (SC == kTiles16 ? r : 16 * r + i) * (uint32_t)(SC == kRows32 ? K / 32 : K / 16) +
+                           (SC == kRows32 ? 4 : 8) * g;
+        int64_t lb = b0 + s0 / steps;
+        int ls = (int)(s0 % steps);
+        auto issue = [&](TileStep<NM, NR> &st) __attribute__((always_inline)) {
+            const int64_t n0 = first_row(lb);
+#pragma unroll
+            for (int w = 0; w < NM; ++w) {
+                src.codes[w] = mat[w].codes + n0 * (K / 2);
+                src.scales[w] = mat[w].scales + (SC == kRows16   ? n0 * (K / 16)
+                                                 : SC == kRows32 ? n0 * (K / 32)
+                                                                 : n0 / 16 * (K / 16));
+            }
+            load_tile<SC, NM, NR>(st, src, step_k(ls));
+            const bool over = ls + 1 == steps;
+            lb += over && lb + 1 < b1 ? 1 : 0;
+            ls = over ? 0 : ls + 1;
+        };
+        // the unit's rows into LDS: a copy for each row of a step, chunk c (16 bytes) of
+        // row r at place c ^ r of its sixteen
+        auto begun = [&]() {
+            __syncthreads();                              // the rows before are done with
+            constexpr int P = NP ? NP : 1, TOK = 16 / P;
+            const int used = n * P;
+            for (int c = wave; c < steps * used; c += NW) {
+                const int s = c / used, q = c - s * used, tk = q / P, r = tk / TOK * 16 + tk % TOK * P + q % P;
+                const int en = entry[tk];
+                const uint16_t *const from = NP ? h + ((q % P) * pairs + (en & 0xFFFF)) * p.F : p.x + (en >> 16) * p.ldx;
+                copy_lds16(from + step_k(s) + 8 * (lane ^ (r & 15)), xs + (s * sh.rows + r) * 1024);
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            const int had = (int)(klo + (steps - 1) * kMoeStep - step_k(steps - 1)) / 8;   // chunks of eight values
+            if (had > 0) {
+                for (int r = wave; r < sh.rows; r += NW)
+                    if (lane < had)
+                        *reinterpret_cast<uint4 *>(xs + ((steps - 1) * sh.rows + r) * 1024 + 16 * (lane ^ (r & 15))) =
+                            make_uint4(0, 0, 0, 0);
+                __syncthreads();
+            }
+        };
+        f32x4 acc[NM][NR][NT];
+        int64_t cb = lb;
+        int cs = ls;
+        bool began = cs == 0;
+        auto clear = [&]() {
+#pragma unroll
+            for (int w = 0; w < NM; ++w)
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) acc[w][r][t] = f32x4{0, 0, 0, 0};
+        };
+        auto place = [&](int o, int w, int r, int t) {
+            return reinterpret_cast<f32x4 *>(part + ((o * 2 + w * NR + r) * NT + t) * 256 + lane * 4);
+        };
+        auto leave = [&]() {
+#pragma unroll
+            for (int w = 0; w < NM; ++w)
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) *place(wave, w, r, t) = acc[w][r][t];
+        };
+        // lane 16 g + i holds row i's sums for weight rows 4 g .. 4 g + 3 of each 16
+        auto finish = [&]() __attribute__((always_inline)) {
+            constexpr int P = NP ? NP : 1, TOK = 16 / P;   // tokens of a tile of rows
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const int own = t * TOK + i / P, en = min(own, n - 1), pr = entry[en] & 0xFFFF;
+                const bool in = i % P == 0 && i / P < TOK && own < n;
+                const float w = NP ? un.weight[(unit >> 10 & 2047) + en] * sv : 0.0f;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int64_t at4 = first_row(cb) + 16 * r + 4 * g;
+                    if (NP == 0) {
+                        if (in && at4 >= cb * (16 * NR))  // (all four: F is a multiple of 16)
+                            finish_hidden4<NM>(p, h, pr, at4, acc[0][r][t], acc[NM - 1][r][t], sv, su);
+                    } else {
+                        f32x4 sum = acc[0][r][t];
+#pragma unroll
+                        for (int k = 1; k < NP; ++k)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) sum[q] += __shfl_down(acc[0][r][t][q], k, 16);
+                        float *const y = p.part + (range * pairs + pr) * p.N + at4;
+                        if (in) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (at4 + q >= cb * (16 * NR)) y[q] = w * sum[q];
+                        }
+                    }
+                }
+            }
+        };
+        auto use = [&](TileStep<NM, NR> &st) __attribute__((always_inline)) {
+            add_tile<SC, NM, NR, NT>(acc, st, xs + cs * sh.rows * 1024, row);
+            if (++cs == steps) {
+                if (began) finish();
+                else leave();
+                clear();
+                cs = 0;
+                ++cb;
+                began = true;
+            }
+        };
+        clear();
+        if (s0 < s1) run_ring<D, TileStep<NM, NR>>(s1 - s0, issue, begun, use);
+        else begun();
+        // a tile that goes on in the next waves
+        const bool open = s0 < s1 && cs != 0;
+        if (open && !began) leave();
+        __syncthreads();
+        if (open && began) {
+            const int64_t over = (cb - b0 + 1) * steps;
+            for (int o = wave + 1; o < NW && all * o / NW < over; ++o) {
+                if (all * o / NW == all * (o + 1) / NW) continue;
+#pragma unroll
+                for (int w = 0; w < NM; ++w)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const f32x4 v = *place(o, w, r, t);
+                            acc[w][r][t] += v;
+                        }
+            }
+            finish();
+        }
+    }
+}
+
+// An output from its pairs' and ranges' sums, in the order of the token's choice.
+__global__ __launch_bounds__(64) void moe_sum_kernel(MoeParams p, int ranges) {
+    __shared__ int64_t from[kMoeSlots];
+    const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x, t = blockIdx.y;
+    const int j = threadIdx.x & (kMoeSlots - 1);
+    const int e = j < p.k ? p.ids[t * p.k + j] : -1;
+    bool first = e >= 0 && e < p.E;                       // an expert chosen again is with its first pair
+    for (int q = 1; q < p.k; ++q) {
+        const int o = __shfl(e, j - q, kMoeSlots);
+        if (j >= q && o == e) first = false;
+    }
+    const uint64_t mask = __ballot(first && threadIdx.x < kMoeSlots);
+    if (first && threadIdx.x < kMoeSlots) from[__builtin_popcountll(mask & ((1ull << j) - 1))] = (t * p.k + j) * p.N;
+    const int count = __builtin_popcountll(mask);
+    __syncthreads();
+    if (n >= p.N) return;
+    float v = 0.0f;
+    for (int r = 0; r < ranges; ++r) {
+        const float *const part = p.part + r * p.T * p.k * p.N + n;
+#pragma unroll 4
+        for (int q = 0; q < count; ++q) v += part[from[q]];
+    }
+    finish_output(p, t, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -305,7 +800,7 @@ __device__ __forceinline__ DownUnits down_lds(uint8_t *lds, const MoeParams &p) 
 
 // The units in LDS, and the sums cleared.
 template <int TOK, int ROWS>
-__device__ __forceinline__ void list_units(const DownUnits &d, const MoeParams &p, const MoePlan &m) {
+__device__ __forceinline__ void list_slots(const DownUnits &d, const MoeParams &p, const MoePlan &m) {
     const int slots = (int)(p.T * p.k < p.E ? p.T * p.k : p.E);
     for (int o = threadIdx.x; o < (int)(blockDim.x >> 6) * p.T * ROWS; o += blockDim.x) d.sums[o] = 0.0f;
     if (threadIdx.x < 64) {
@@ -328,28 +823,26 @@ __device__ __forceinline__ void list_units(const DownUnits &d, const MoeParams &
 }
 
 template <int ROWS>
-__device__ __forceinline__ void join_waves(const DownUnits &d, const MoeParams &p, int64_t n0) {
+__device__ __forceinline__ void join_waves(const float *sums, const MoeParams &p, int64_t n0) {
     __syncthreads();
     const int nw = blockDim.x >> 6;
     for (int o = threadIdx.x; o < (int)p.T * ROWS; o += blockDim.x) {
         const int64_t t = o / ROWS, n = n0 + o % ROWS;
         if (n >= p.N) continue;
         float v = 0.0f;
-        for (int w = 0; w < nw; ++w) v += d.sums[w * (int)p.T * ROWS + o];
-        if (p.r) v += value_at(p.r, t * p.ldr + n, p.bf16_out);
-        if (p.bf16_out) static_cast<uint16_t *>(p.y)[t * p.ldy + n] = (uint16_t)pk_bf16(v, v);
-        else static_cast<float *>(p.y)[t * p.ldy + n] = v;
+        for (int w = 0; w < nw; ++w) v += sums[w * (int)p.T * ROWS + o];
+        finish_output(p, t, n, v);
     }
 }
 
 // NP parts a value, TOK tokens of a unit: TOK NP <= 4 rows of the 4 x 4 x 4 products.
 template <int SC, int NP, int TOK, int R>
-__global__ __launch_bounds__(64 * kMoeSplit) void moe_down_few_kernel(MoeParams p) {
+__global__ __launch_bounds__(64 * kSplit) void moe_down_few_kernel(MoeParams p) {
     constexpr int ROWS = 4 * R, TT = TOK * NP;
     extern __shared__ __align__(16) uint8_t lds[];
     const DownUnits d = down_lds(lds, p);
     const MoePlan m = plan_of(p);
-    list_units<TOK, ROWS>(d, p, m);
+    list_slots<TOK, ROWS>(d, p, m);
     const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t n0 = (int64_t)blockIdx.x * ROWS;
@@ -407,12 +900,12 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_down_few_kernel(MoeParams 
             }
         }
     }
-    join_waves<ROWS>(d, p, n0);
+    join_waves<ROWS>(d.sums, p, n0);
 }
 
 // The same with 16 x 16 x 32 products: 16 / NP tokens a unit.
 template <int SC, int NP>
-__global__ __launch_bounds__(64 * kMoeSplit) void moe_down_tile_kernel(MoeParams p) {
+__global__ __launch_bounds__(64 * kSplit) void moe_down_tile_kernel(MoeParams p) {
     constexpr int ROWS = 16, TOK = 16 / NP;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
@@ -420,7 +913,7 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_down_tile_kernel(MoeParams
     uint8_t *const xl = lds + wave * 4096;                // the waves' hidden values come first
     const DownUnits d = down_lds(lds + nw * 4096, p);
     const MoePlan m = plan_of(p);
-    list_units<TOK, ROWS>(d, p, m);
+    list_slots<TOK, ROWS>(d, p, m);
     const int i = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * ROWS;
     const int64_t full = p.F / kTileK, steps = (p.F + kTileK - 1) / kTileK, total = *d.units * steps;
@@ -490,7 +983,7 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_down_tile_kernel(MoeParams
             for (int e4 = 0; e4 < 4; ++e4) to[e4] += en.weight * (sum[e4] * sd);
         }
     }
-    join_waves<ROWS>(d, p, n0);
+    join_waves<ROWS>(d.sums, p, n0);
 }
 
 // ---------------------------------------------------------------------------
@@ -499,14 +992,44 @@ __global__ __launch_bounds__(64 * kMoeSplit) void moe_down_tile_kernel(MoeParams
 template <auto Kernel>
 hipError_t launch_down(const MoeParams &p, int rows, size_t wave_bytes, hipStream_t s) {
     const int64_t pairs = p.T * p.k;
-    const size_t shm = 16 + (pairs + 3) / 4 * 16 + kMoeSplit * (p.T * rows * 4 + wave_bytes);
+    const size_t shm = 16 + (pairs + 3) / 4 * 16 + kSplit * (p.T * rows * 4 + wave_bytes);
     static const bool attr_set = [rows, wave_bytes] {
-        const int most = 16 + 64 * kMoeSlots * 4 + kMoeSplit * (64 * rows * 4 + (int)wave_bytes);
+        const int most = 16 + 64 * kMoeSlots * 4 + kSplit * (64 * rows * 4 + (int)wave_bytes);
         (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize, most);
         return true;
     }();
     (void)attr_set;
-    hipLaunchKernelGGL(Kernel, dim3((unsigned)((p.N + rows - 1) / rows)), dim3(64 * kMoeSplit), shm, s, p);
+    hipLaunchKernelGGL(Kernel, dim3((unsigned)((p.N + rows - 1) / rows)), dim3(64 * kSplit), shm, s, p);
+    return hipGetLastError();
+}
+
+// Streaming pays from about 50 MB of codes of the experts that can be chosen: below it
+// the lists and the third launch cost more than the earlier forms' uneven loads.
+// Measured (streaming against not): 20 MB, 5 tokens, 25.7 and 17.4 us; 50 MB, 8
+// tokens, 33.2 and 29.9, 16 tokens (MXFP4) 33.6 and 33.3, 64 tokens 52.5 and 60.9;
+// 100 MB, 8 tokens, 37.4 and 45.0, 64 tokens 62.5 and 103; 604 MB, 5 tokens, 85.5 and 129.
+// It needs a whole step of each K, a tile's rows, and room in LDS for four rows of x.
+bool streams(const MoeParams &p) {
+    const int64_t codes = moe_slots(p.T, p.k, p.E) * ((p.gated ? 2 : 1) * p.F * p.K + p.N * p.F) / 2;
+    return codes > (48 << 20) && p.K >= kMoeStep && p.F >= kMoeStep && p.N >= 32 &&
+           moe_up_shape(p.T, p.k, p.E, p.K).rows > 0;
+}
+
+// Steps in flight beside the one in use: two for NVFP4 (64 tokens, 118 us against 123
+// with one), one for MXFP4, whose steps are short (16 tokens, 65 us against 68 with two).
+template <int SC>
+constexpr int kRing = SC == kRows32 ? 1 : 2;
+
+template <auto Kernel>
+hipError_t launch_stream(const MoeParams &p, const MoeShape &sh, hipStream_t s) {
+    const int64_t shm = moe_tile_lds(p.T, p.k, p.E, sh);
+    static const bool attr_set = [] {
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                  kMoeLds);
+        return true;
+    }();
+    (void)attr_set;
+    hipLaunchKernelGGL(Kernel, dim3((unsigned)device_cus(s)), dim3(64 * kMoeTileWaves), (size_t)shm, s, p, sh);
     return hipGetLastError();
 }
 
@@ -514,7 +1037,7 @@ template <int SC, int NM, int TT>
 hipError_t up_few(const MoeParams &p, hipStream_t s) {
     constexpr int R = 4 / NM;
     const dim3 grid((unsigned)((p.F + 4 * R - 1) / (4 * R)), (unsigned)moe_slots(p.T, p.k, p.E));
-    hipLaunchKernelGGL((moe_up_few_kernel<SC, NM, TT, R>), grid, dim3(64 * kMoeSplit), 0, s, p);
+    hipLaunchKernelGGL((moe_up_few_kernel<SC, NM, TT, R>), grid, dim3(64 * kUpFewSplit), 0, s, p);
     return hipGetLastError();
 }
 
@@ -523,8 +1046,20 @@ hipError_t up(const MoeParams &p, hipStream_t s) {
     if (p.T == 1) return up_few<SC, NM, 1>(p, s);
     if (p.T == 2) return up_few<SC, NM, 2>(p, s);
     if (p.T <= 4) return up_few<SC, NM, 4>(p, s);
+    if (streams(p))
+        return launch_stream<moe_stream_kernel<SC, NM, 2 / NM, 0, 1, kRing<SC>>>(p, moe_up_shape(p.T, p.k, p.E, p.K), s);
     const dim3 grid((unsigned)((p.F + 15) / 16), (unsigned)moe_slots(p.T, p.k, p.E));
-    hipLaunchKernelGGL((moe_up_tile_kernel<SC, NM, 1>), grid, dim3(64 * kMoeSplit), 0, s, p);
+    hipLaunchKernelGGL((moe_up_tile_kernel<SC, NM, 1>), grid, dim3(64 * kSplit), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int SC, int NP>
+hipError_t down_stream(const MoeParams &p, hipStream_t s) {
+    const MoeShape sh = moe_down_shape(p.T, p.k, p.E, p.F);
+    const hipError_t e = sh.rows == 32 ? launch_stream<moe_stream_kernel<SC, 1, 2, NP, 2, kRing<SC>>>(p, sh, s)
+                                       : launch_stream<moe_stream_kernel<SC, 1, 2, NP, 1, kRing<SC>>>(p, sh, s);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((p.N + 63) / 64), (unsigned)p.T), dim3(64), 0, s, p, sh.ranges);
     return hipGetLastError();
 }
 
@@ -535,6 +1070,7 @@ hipError_t down(const MoeParams &p, hipStream_t s) {
         if (p.T == 1) return launch_down<moe_down_few_kernel<SC, 2, 1, 4>>(p, 16, 0, s);
         return launch_down<moe_down_few_kernel<SC, 2, 2, 4>>(p, 16, 0, s);
     }
+    if (streams(p)) return p.bf16_out ? down_stream<SC, 2>(p, s) : down_stream<SC, 3>(p, s);
     if (p.bf16_out) return launch_down<moe_down_tile_kernel<SC, 2>>(p, 16, 4096, s);
     return launch_down<moe_down_tile_kernel<SC, 3>>(p, 16, 4096, s);
 }

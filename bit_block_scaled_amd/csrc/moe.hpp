@@ -28,16 +28,58 @@ struct MoeParams {
     void *y;                           // T x N
     int64_t ldy;
     int bf16_out;
-    uint8_t *ws;                       // moe_ws_bytes
+    uint8_t *ws;                       // moe_ws_bytes; the hidden values first
+    float *part;                       // in ws, behind them: outputs of a range of a pair
 };
 
-// Bytes of workspace: the routing and the hidden values.
-inline int64_t moe_slots(int64_t T, int64_t k, int64_t E) { return T * k < E ? T * k : E; }
-inline int64_t moe_plan_bytes(int64_t T, int64_t k, int64_t E) {
-    return (moe_slots(T, k, E) * (8 + T * (int64_t)sizeof(MoeEntry)) + 15) / 16 * 16;
+// ---------------------------------------------------------------------------
+// The tile kernels' shapes
+// ---------------------------------------------------------------------------
+constexpr int kMoeTileWaves = 8;
+constexpr int kMoeStep = 512;                                      // K values of a step
+constexpr int kMoeLds = 160 * 1024;                                // of a CU
+
+// How a tile kernel divides its K: ranges of `range` values (a multiple of a step where
+// there are several), of which `rows` (32, 16, 8 or 4) rows fit LDS.
+struct MoeShape {
+    int64_t range;
+    int ranges, rows;
+};
+
+// LDS of a tile kernel: the rows, the waves' sums (for each 16 rows), the units.
+__host__ __device__ inline int64_t moe_rows_bytes(const MoeShape &s) {
+    return (s.range + kMoeStep - 1) / kMoeStep * s.rows * 1024;
 }
-inline int64_t moe_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t F) {
-    return moe_plan_bytes(T, k, E) + 3 * T * k * F * 2;
+__host__ __device__ constexpr int64_t moe_sums_bytes(int tiles) { return kMoeTileWaves * 512 * 4 * tiles; }
+inline int64_t moe_units_bytes(int64_t T, int64_t k, int64_t E) { return 32 + E * 12 + T * k * 16; }
+inline int64_t moe_tile_lds(int64_t T, int64_t k, int64_t E, const MoeShape &s) {
+    return moe_rows_bytes(s) + moe_sums_bytes((s.rows + 15) / 16) + moe_units_bytes(T, k, E);
+}
+// Up projection: an activation needs all of K, so the rows are as many as fit (0: too few).
+inline MoeShape moe_up_shape(int64_t T, int64_t k, int64_t E, int64_t K) {
+    MoeShape s{K, 1, 16};
+    while (s.rows >= 4 && moe_tile_lds(T, k, E, s) > kMoeLds) s.rows /= 2;
+    if (s.rows < 4) s.rows = 0;
+    return s;
+}
+// Down projection: as few ranges as leave room for two tiles of sixteen rows.
+inline MoeShape moe_down_shape(int64_t T, int64_t k, int64_t E, int64_t F) {
+    MoeShape s{F, 1, T > 8 ? 32 : 16};
+    while (moe_tile_lds(T, k, E, s) > kMoeLds) {
+        ++s.ranges;
+        s.range = (F + kMoeStep * s.ranges - 1) / (kMoeStep * s.ranges) * kMoeStep;
+    }
+    s.ranges = (int)((F + s.range - 1) / s.range);
+    return s;
+}
+
+// Bytes of workspace: the hidden values, then the routing or the pairs' outputs.
+inline int64_t moe_slots(int64_t T, int64_t k, int64_t E) { return T * k < E ? T * k : E; }
+inline int64_t moe_hidden_bytes(int64_t T, int64_t k, int64_t F) { return 3 * T * k * F * 2; }
+inline int64_t moe_ws_bytes(int64_t T, int64_t k, int64_t E, int64_t F, int64_t N) {
+    const int64_t plan = moe_slots(T, k, E) * (8 + T * (int64_t)sizeof(MoeEntry));
+    const int64_t part = moe_down_shape(T, k, E, F).ranges * T * k * N * 4;
+    return moe_hidden_bytes(T, k, F) + (plan > part ? plan : part);
 }
 
 hipError_t launch_moe(const MoeParams &p, bool mxfp4, hipStream_t s);

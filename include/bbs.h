@@ -465,7 +465,7 @@ int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t 
  * and in three (24) for FP32 ones; they must be below 2^127.  The sums' order
  * depends on sizes, format and routing alone; a token's answer then differs from
  * what it gets beside other tokens by the rounding of FP32 sums.
- * ws: nvfp4_moe_ws_bytes(tokens, k, experts, F) bytes of device workspace, 16-byte
+ * ws: nvfp4_moe_ws_bytes(tokens, k, experts, F, N) bytes of device workspace, 16-byte
  * aligned, not kept; calls that overlap in time need one each.
  * Errors: BBS_EINVAL; BBS_ENOTSUP for weights with a per-row decode scale or with
  * different tile2d, or for 2^24 features or more. */
@@ -475,7 +475,7 @@ int nvfp4_moe_gemv(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t ldx, 
                    int32_t y_dtype, int64_t ldy, void *stream);
 
 /* Bytes of workspace of such a call (negative: BBS_EINVAL). */
-int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden);
+int64_t nvfp4_moe_ws_bytes(int64_t tokens, int32_t k, int32_t experts, int64_t hidden, int64_t features);
 
 /* Name of a status code. */
 const char *bbs_strerror(int status);

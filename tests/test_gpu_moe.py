@@ -120,6 +120,21 @@ CASES = [
     (64, 1024, 32, 32, 32, 16, "mxfp4", False, False, "gelu", True, True, "bf16", "", 0),
     (64, 10, 4, 1024, 640, 32, "nvfp4", False, False, "silu", True, True, "bf16", "one", 0),
     (40, 16, 4, 64, 64, 64, "nvfp4", True, True, "silu", True, True, "f32", "none", 8),
+    # five tokens on, with weights enough for the streaming kernels
+    (5, 64, 8, 544, 1568, 1040, "nvfp4", False, False, "silu", True, False, "bf16", "", 0),
+    (8, 64, 8, 528, 1552, 1040, "nvfp4", False, True, "gelu", True, True, "f32", "", 8),
+    (9, 100, 12, 544, 608, 1568, "mxfp4", False, True, "gelu", True, True, "f32", "dropped", 8),
+    (24, 6, 3, 2064, 4624, 2080, "nvfp4", True, True, "silu", True, True, "f32", "", 0),
+    (13, 8, 2, 5136, 1040, 2064, "nvfp4", False, True, "silu", True, False, "bf16", "", 0),
+    (64, 6, 2, 4640, 2080, 2085, "mxfp4", False, False, "gelu", True, True, "f32", "", 8),
+    (11, 8, 1, 512, 16400, 2064, "nvfp4", False, True, "silu", True, False, "bf16", "", 0),
+    (6, 8, 2, 512, 40960, 48, "nvfp4", True, False, "", True, True, "bf16", "", 0),
+    (33, 64, 8, 1552, 1552, 160, "nvfp4", True, True, "silu", True, True, "bf16", "", 8),
+    (64, 1024, 32, 512, 544, 32, "mxfp4", False, True, "silu", True, False, "bf16", "", 0),
+    (40, 48, 32, 1040, 1552, 1040, "nvfp4", False, True, "silu", False, True, "bf16", "twice", 0),
+    (64, 16, 4, 2064, 2576, 2064, "nvfp4", False, False, "", True, True, "f32", "one", 0),
+    (16, 64, 3, 1056, 1056, 1056, "mxfp4", False, True, "silu", True, True, "f32", "none", 8),
+    (17, 64, 8, 1056, 1568, 45, "mxfp4", False, True, "gelu", True, False, "bf16", "", 0),
 ]
 
 
@@ -140,7 +155,7 @@ def test_moe(bbs, T, E, k, F, K, N, fmt, tile2d, gated, act, weighted, res, out,
     within(y, ref, err, bool(flag), "y")
     untouched(full, T, N, "y")
     # again, into the residual itself and with a workspace that holds other values: the same bits
-    ws = bbs.moe_workspace(T, k, E, F, dev()).fill_(0xFF)
+    ws = bbs.moe_workspace(T, k, E, F, N, dev()).fill_(0xFF)
     again = r.clone(memory_format=torch.contiguous_format) if res else torch.empty((T, N), dtype=dtype, device=dev())
     bbs.nvfp4_moe_gemv(f, x, ids, weights, E, Wg, Wu, Wd, again, flag, act=ACTS[act], residual=again if res else None, ws=ws)
     assert torch.equal(again, y)
@@ -151,8 +166,9 @@ def test_moe(bbs, T, E, k, F, K, N, fmt, tile2d, gated, act, weighted, res, out,
 def test_tokens_do_not_mix(bbs):
     """NaN and infinite tokens, and NaN weights of experts nobody chose, stay where they are."""
     announce("moe: NaN")
-    for T, E, k, fmt in ((4, 16, 3, "nvfp4"), (24, 8, 2, "mxfp4"), (2, 9, 2, "mxfp4")):
-        F, K, N = 96, 160, 64
+    for T, E, k, fmt, wide in ((4, 16, 3, "nvfp4", 1), (24, 8, 2, "mxfp4", 1), (2, 9, 2, "mxfp4", 1),
+                               (24, 8, 2, "mxfp4", 33), (40, 9, 3, "nvfp4", 33)):
+        F, K, N = 96 * wide, 160 * wide, 64
         Wg, Wu, Wd = (experts(bbs, fmt, E, r, c, False, i) for i, (r, c) in enumerate(((F, K), (F, K), (N, F))))
         ids = routing(T, E - 1, k, "", 5)                               # the last expert is never chosen
         if fmt == "mxfp4":
@@ -201,8 +217,8 @@ def test_weights_beyond_32_bits(bbs):
         within(y, *layer64(bbs, x, ids, None, E, None, Wu, Wd, "gelu", None, False), False, "y")
 
 
-def problem(bbs, T, seed):
-    E, k, F, K, N = 16, 4, 208, 272, 160
+def problem(bbs, T, seed, wide=1):
+    E, k, F, K, N = 16, 4, 208 * wide, 272 * wide, 160 * wide
     return {"x": normal((T, K), torch.bfloat16, seed), "ids": routing(T, E, k, "dropped", seed),
             "w": torch.softmax(normal((T, k), torch.float32, seed + 1), 1), "r": normal((T, N), torch.bfloat16, seed + 2),
             "W": [experts(bbs, "nvfp4", E, r, c, True, seed + i) for i, (r, c) in enumerate(((F, K), (F, K), (N, F)))]}
@@ -215,12 +231,12 @@ def run(bbs, q, stream=None):
     return y, z
 
 
-@pytest.mark.parametrize("T", [1, 3, 20])
-def test_streams_and_graphs(bbs, T):
+@pytest.mark.parametrize("T,wide", [(1, 1), (3, 1), (20, 1), (20, 10)])
+def test_streams_and_graphs(bbs, T, wide):
     """On a side stream, and captured and replayed with new tokens and another
     routing, with eager calls between the replays."""
-    announce(f"moe: stream and graph, {T} tokens")
-    q = problem(bbs, T, 1)
+    announce(f"moe: stream and graph, {T} tokens, {wide}")
+    q = problem(bbs, T, 1, wide)
     eager = run(bbs, q)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -241,9 +257,10 @@ def test_streams_and_graphs(bbs, T):
         assert same(eager, cap), i
 
 
-def test_calls_at_once(bbs):
+@pytest.mark.parametrize("wide", [1, 10])
+def test_calls_at_once(bbs, wide):
     announce("moe: two streams at once")
-    probs = problem(bbs, 20, 10), problem(bbs, 2, 20)
+    probs = problem(bbs, 20, 10, wide), problem(bbs, 2, 20)
     alone = [run(bbs, q) for q in probs]
     torch.cuda.synchronize()
     both = []
@@ -256,11 +273,12 @@ def test_calls_at_once(bbs):
     assert same(alone[0], both[0]) and same(alone[1], both[1])
 
 
-def test_two_graphs_of_one_workspace(bbs):
+@pytest.mark.parametrize("wide", [1, 10])
+def test_two_graphs_of_one_workspace(bbs, wide):
     """Two captured calls that share a workspace, replayed in turn on one stream."""
     announce("moe: two graphs, one workspace")
-    a, b = problem(bbs, 5, 1), problem(bbs, 5, 30)
-    ws = bbs.moe_workspace(5, 4, 16, 208, dev())
+    a, b = problem(bbs, 5, 1, wide), problem(bbs, 5, 30, wide)
+    ws = bbs.moe_workspace(5, 4, 16, 208 * wide, 160 * wide, dev())
 
     def call(q):
         y = torch.empty_like(q["r"])

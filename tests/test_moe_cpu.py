@@ -76,14 +76,14 @@ def test_errors():
 
 def test_workspace_size():
     size = L.nvfp4_moe_ws_bytes
-    assert size(1, 8, 64, 1536) >= 3 * 8 * 1536 * 2
-    assert size(64, 32, 1024, 1536) % 16 == 0
-    for a in ((0, 8, 64, 64), (65, 8, 64, 64), (1, 0, 64, 64), (1, 33, 64, 64), (1, 8, 0, 64), (1, 8, 1025, 64),
-              (1, 8, 64, 0), (1, 8, 64, 1 << 24)):
+    assert size(1, 8, 64, 1536, 4096) >= 3 * 8 * 1536 * 2
+    assert size(64, 32, 1024, 1536, 4096) % 4 == 0
+    for a in ((0, 8, 64, 64, 64), (65, 8, 64, 64, 64), (1, 0, 64, 64, 64), (1, 33, 64, 64, 64), (1, 8, 0, 64, 64),
+              (1, 8, 1025, 64, 64), (1, 8, 64, 0, 64), (1, 8, 64, 1 << 24, 64), (1, 8, 64, 64, 0), (1, 8, 64, 64, 1 << 24)):
         assert size(*a) == EINVAL
-    assert bbs.moe_workspace(2, 2, 4, 32, "cpu").numel() == size(2, 2, 4, 32)
+    assert bbs.moe_workspace(2, 2, 4, 32, 48, "cpu").numel() == size(2, 2, 4, 32, 48)
     with pytest.raises(bbs.BbsError):
-        bbs.moe_workspace(65, 2, 4, 32, "cpu")
+        bbs.moe_workspace(65, 2, 4, 32, 48, "cpu")
 
 
 T, k, E, K, F, N = 3, 2, 4, 64, 32, 48
