@@ -169,13 +169,25 @@ __global__ __launch_bounds__(256) void bias_act_bwd_kernel(BiasActBwdParams p, i
     }
 }
 
+// 64 columns a workgroup; wave w adds every fourth range from w on, with its loads in
+// flight together.
 template <bool BF16>
-__global__ __launch_bounds__(64) void bias_sum_kernel(const float *part, int64_t N, int parts, void *db) {
-    const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-    if (n >= N) return;
-    float v = part[n];
-    for (int i = 1; i < parts; ++i) v += part[i * N + n];
-    store_db<BF16>(db, n, v);
+__global__ __launch_bounds__(256) void bias_sum_kernel(const float *part, int64_t N, int parts, void *db) {
+    __shared__ float sums[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 64 + lane;
+    const float *const from = part + min(n, N - 1);
+    float v = 0.0f;
+    for (int i = w; i < parts; i += 32) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = from[min(i + 4 * j, parts - 1) * N];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v += i + 4 * j < parts ? x[j] : 0.0f;
+    }
+    sums[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && n < N) store_db<BF16>(db, n, sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
 }
 
 template <int TM, int NS, int G>
@@ -212,8 +224,8 @@ hipError_t launch_bias_act_bwd(const BiasActBwdParams &p, hipStream_t s) {
     else hipLaunchKernelGGL((bias_act_bwd_kernel<kActNone>), grid, dim3(256), 0, s, p, rows, (int)parts);
     if (p.db && parts > 1) {
         const dim3 g2((unsigned)((p.N + 63) / 64));
-        if (p.db_bf16) hipLaunchKernelGGL(bias_sum_kernel<true>, g2, dim3(64), 0, s, p.part, p.N, (int)parts, p.db);
-        else hipLaunchKernelGGL(bias_sum_kernel<false>, g2, dim3(64), 0, s, p.part, p.N, (int)parts, p.db);
+        if (p.db_bf16) hipLaunchKernelGGL(bias_sum_kernel<true>, g2, dim3(256), 0, s, p.part, p.N, (int)parts, p.db);
+        else hipLaunchKernelGGL(bias_sum_kernel<false>, g2, dim3(256), 0, s, p.part, p.N, (int)parts, p.db);
     }
     return hipGetLastError();
 }
