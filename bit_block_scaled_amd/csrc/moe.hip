@@ -338,34 +338,38 @@ __device__ __forceinline__ void finish_output(const MoeParams &p, int64_t t, int
 // Streaming kernels: 16 x 16 x 32 products, sixteen tokens (or rows of parts of hidden
 // values) by sixteen weight rows, 512 K values a step.
 //
-// One workgroup of eight waves a CU, two a SIMD, with 256 registers each for the
-// weights in flight (four a SIMD with half of them measured the same, and the rows
-// in LDS leave no room for them in the up projection).  Each workgroup lists the units
-// first: an expert and up to a tile's rows of its tokens, in ascending order.
+// One workgroup of eight waves a CU.  Each lists the units first: an expert and up to
+// a tile's rows of its tokens, in ascending order.
 //
-// Bound, at 64 tokens, by the expansion of the codes: two vector instructions a code
-// and half of one for the exchange of lanes (counters: vector units 70% busy, L1, LDS
-// and the matrix units below 25%); MXFP4 codes, half an instruction each, by the loads.
+// Bound by the loads together with the expansion of the codes (NVFP4: two vector
+// instructions a code and half of one for the exchange of lanes, vector units 65%
+// busy; MXFP4: half an instruction and the exchange).  Up projections of 4096 to 1536,
+// with the weights that a second unit of an expert reads again: 64 tokens, NVFP4, 464 MB
+// in 113 us (4.1 TB/s); 16 tokens, MXFP4, 307 MB in 66 us (4.7); a plain read of such
+// sizes reaches 5.7 to 6.3 TB/s.  About 10 us of each are the lists, the first loads
+// and the last units.
 // ---------------------------------------------------------------------------
 struct Units {
-    uint64_t *mask;                    // the tokens of each expert
-    int32_t *first;                    // its first entry
-    int32_t *ids, *entry;              // of each pair; entry: pair | token << 16
+    int32_t *entry;                    // pair | token << 16
     float *weight;                     // of each entry
     int32_t *unit;                     // expert | first entry << 10 | entries << 21
     int32_t *count;                    // the units
+    // while they are listed, where the rows come afterwards
+    uint64_t *mask;                    // the tokens of each expert
+    int32_t *first;                    // its first entry
+    int32_t *ids;                      // of each pair
 };
 
-__device__ __forceinline__ Units units_at(uint8_t *lds, const MoeParams &p) {
+__device__ __forceinline__ Units units_at(uint8_t *lds, uint8_t *scratch, const MoeParams &p) {
     const int pairs = (int)p.T * p.k;
     Units u;
-    u.mask = reinterpret_cast<uint64_t *>(lds);
-    u.first = reinterpret_cast<int32_t *>(u.mask + p.E);
-    u.ids = u.first + p.E;
-    u.entry = u.ids + pairs;
+    u.entry = reinterpret_cast<int32_t *>(lds);
     u.weight = reinterpret_cast<float *>(u.entry + pairs);
     u.unit = reinterpret_cast<int32_t *>(u.weight + pairs);
     u.count = u.unit + pairs;
+    u.mask = reinterpret_cast<uint64_t *>(scratch);
+    u.first = reinterpret_cast<int32_t *>(u.mask + p.E);
+    u.ids = u.first + p.E;
     return u;
 }
 
@@ -570,7 +574,7 @@ __device__ __forceinline__ float scalar(float v) {
 // after another's, are cut into even parts for the waves.  A wave that comes into a
 // tile behind its first step leaves its sums in LDS for the one that began it.
 template <int SC, int NM, int NR, int NP, int NT, int D>
-__global__ __launch_bounds__(64 * kMoeTileWaves, 2) void moe_stream_kernel(MoeParams p, MoeShape sh) {
+__global__ __launch_bounds__(64 * kMoeTileWaves, kMoeTileWaves / 4) void moe_stream_kernel(MoeParams p, MoeShape sh) {
     static_assert(NM * NR == 2, "a tile's sums fill a wave's buffer");
     constexpr int NW = kMoeTileWaves;
     extern __shared__ __align__(16) uint8_t lds[];
@@ -578,7 +582,7 @@ __global__ __launch_bounds__(64 * kMoeTileWaves, 2) void moe_stream_kernel(MoePa
     const int64_t most = moe_rows_bytes(sh);
     uint8_t *const xs = lds;                                                   // [step][row][1024 bytes]
     float *const part = reinterpret_cast<float *>(lds + most);
-    const Units un = units_at(lds + most + moe_sums_bytes(NT), p);
+    const Units un = units_at(lds + most + moe_sums_bytes(NT), lds, p);
     const int tok = NP ? sh.rows / 16 * (16 / (NP ? NP : 1)) : sh.rows;
     list_units(un, p, tok);
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
@@ -1012,7 +1016,7 @@ hipError_t launch_down(const MoeParams &p, int rows, size_t wave_bytes, hipStrea
 bool streams(const MoeParams &p) {
     const int64_t codes = moe_slots(p.T, p.k, p.E) * ((p.gated ? 2 : 1) * p.F * p.K + p.N * p.F) / 2;
     return codes > (48 << 20) && p.K >= kMoeStep && p.F >= kMoeStep && p.N >= 32 &&
-           moe_up_shape(p.T, p.k, p.E, p.K).rows > 0;
+           moe_up_shape(p.T, p.k, p.K).rows > 0;
 }
 
 // Steps in flight beside the one in use: two for NVFP4 (64 tokens, 118 us against 123
@@ -1022,7 +1026,7 @@ constexpr int kRing = SC == kRows32 ? 1 : 2;
 
 template <auto Kernel>
 hipError_t launch_stream(const MoeParams &p, const MoeShape &sh, hipStream_t s) {
-    const int64_t shm = moe_tile_lds(p.T, p.k, p.E, sh);
+    const int64_t shm = moe_tile_lds(p.T, p.k, sh);
     static const bool attr_set = [] {
         (void)hipFuncSetAttribute(reinterpret_cast<const void *>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                   kMoeLds);
@@ -1047,7 +1051,7 @@ hipError_t up(const MoeParams &p, hipStream_t s) {
     if (p.T == 2) return up_few<SC, NM, 2>(p, s);
     if (p.T <= 4) return up_few<SC, NM, 4>(p, s);
     if (streams(p))
-        return launch_stream<moe_stream_kernel<SC, NM, 2 / NM, 0, 1, kRing<SC>>>(p, moe_up_shape(p.T, p.k, p.E, p.K), s);
+        return launch_stream<moe_stream_kernel<SC, NM, 2 / NM, 0, 1, kRing<SC>>>(p, moe_up_shape(p.T, p.k, p.K), s);
     const dim3 grid((unsigned)((p.F + 15) / 16), (unsigned)moe_slots(p.T, p.k, p.E));
     hipLaunchKernelGGL((moe_up_tile_kernel<SC, NM, 1>), grid, dim3(64 * kSplit), 0, s, p);
     return hipGetLastError();
@@ -1055,7 +1059,7 @@ hipError_t up(const MoeParams &p, hipStream_t s) {
 
 template <int SC, int NP>
 hipError_t down_stream(const MoeParams &p, hipStream_t s) {
-    const MoeShape sh = moe_down_shape(p.T, p.k, p.E, p.F);
+    const MoeShape sh = moe_down_shape(p.T, p.k, p.F);
     const hipError_t e = sh.rows == 32 ? launch_stream<moe_stream_kernel<SC, 1, 2, NP, 2, kRing<SC>>>(p, sh, s)
                                        : launch_stream<moe_stream_kernel<SC, 1, 2, NP, 1, kRing<SC>>>(p, sh, s);
     if (e != hipSuccess) return e;
