@@ -400,6 +400,13 @@ def _on_current(stream, *tensors):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _used_on(ws, stream):
+    """A workspace of this call alone, kept from reuse until the stream is past the call: the
+    allocator knows it as the current stream's."""
+    if stream is not None:
+        ws.record_stream(stream)
+
+
 def nvfp4_gated_gemm(A, Wg, Wu, H, h_dtype, act=ACT_SILU, g_ckpt=None, u_ckpt=None, ldh=None,
                      stream=None):
     """H = act(A * Wg^T) * (A * Wu^T) in one kernel (NVFP4Tensors A [M, K], Wg and
@@ -535,8 +542,9 @@ def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=Non
     elif act != ACT_NONE:
         raise ValueError("an activation's backward pass needs z_ckpt")
     b, b_dtype = _vector(dbias, N, "dbias")
+    own = dbias is not None and ws is None
     if dbias is not None:
-        if ws is None:
+        if own:
             ws = torch.empty((BIAS_PARTS * N,), dtype=torch.float32, device=dY.device)
         elif ws.dtype != torch.float32 or not ws.is_contiguous() or ws.numel() < BIAS_PARTS * N:
             raise ValueError(f"ws must hold {BIAS_PARTS * N} adjacent float32 values")
@@ -545,6 +553,8 @@ def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=Non
     zd = z_ckpt.desc() if z_ckpt is not None else None
     _check(lib.mxfp8_bias_act_bwd(_ptr(dY), M, N, ldy, C.byref(zd) if zd is not None else None, act, _ptr(dZ), ldz,
                                   b, b_dtype, _ptr(ws), s))
+    if own:
+        _used_on(ws, stream)
 
 
 def nvfp4_gemv_bias_act(fmt, x, W, y, y_dtype, bias=None, act=ACT_NONE, residual=None, ldy=None, ldr=None,
@@ -608,7 +618,8 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
         tensors.append(residual)
     if T == 1:
         ldx = K                          # a single row's stride may be anything in PyTorch
-    if ws is None:
+    own = ws is None
+    if own:
         ws = moe_workspace(T, k, experts, F, N, x.device)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < lib.nvfp4_moe_ws_bytes(T, k, experts, F, N):
         raise ValueError("ws must be a moe_workspace of the call's sizes")
@@ -616,3 +627,5 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
     _check(lib.nvfp4_moe_gemv(fmt, x.data_ptr(), T, ldx, ids.data_ptr(), _ptr(weights), k, experts,
                               None if Wg is None else Wg.packed(), Wu.packed(), Wd.packed(), act, _ptr(residual),
                               ldr or 0, ws.data_ptr(), y.data_ptr(), y_dtype, ldy, s))
+    if own:
+        _used_on(ws, stream)

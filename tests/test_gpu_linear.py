@@ -400,3 +400,25 @@ def test_calls_at_once(bbs):
         both.append(got)
     torch.cuda.synchronize()
     assert same(alone[0], both[0]) and same(alone[1], both[1])
+
+
+def test_own_workspace_on_another_stream(bbs, monkeypatch):
+    """A workspace the call allocates for a given stream is not handed out again while that
+    stream has yet to run the call."""
+    announce("bias gradient: own workspace, other stream")
+    dy, db = normal((2048, 512), torch.bfloat16, 1), torch.empty((512,), device=dev())
+    bbs.mxfp8_bias_act_bwd(dy, None, bbs.ACT_NONE, None, db)
+    want = db.clone()
+    made, keep = [], bbs._used_on
+    monkeypatch.setattr(bbs, "_used_on", lambda ws, stream: made.append((ws.data_ptr(), ws.numel())) or keep(ws, stream))
+    a, s = torch.ones((4096, 4096), device=dev()), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            a @ a                                                       # milliseconds
+    bbs.mxfp8_bias_act_bwd(dy, None, bbs.ACT_NONE, None, db.zero_(), stream=s)
+    other = torch.empty((made[0][1],), device=dev())
+    busy = not s.query()
+    assert other.data_ptr() != made[0][0]
+    torch.cuda.synchronize()
+    assert busy and torch.equal(db, want)

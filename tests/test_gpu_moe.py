@@ -314,3 +314,28 @@ def test_one_expert_is_the_few_token_block(bbs):
     bbs.nvfp4_moe_gemv(0, x, ids, None, 1, *W, y, 0)
     room = (2.0 ** -8 + 600 * ULP) * (h.double().abs() @ nv64(W[2]).abs().t()) + 2.0 ** -20
     assert bool(((y - z).abs().double() <= room).all())
+
+
+def test_own_workspace_on_another_stream(bbs, monkeypatch):
+    """A workspace the call allocates for a given stream is not handed out again while that
+    stream has yet to run the call."""
+    announce("moe: own workspace, other stream")
+    q = problem(bbs, 20, 1)
+    eager = run(bbs, q)
+    made = []
+    make = bbs.moe_workspace
+    monkeypatch.setattr(bbs, "moe_workspace", lambda *a: made.append(make(*a)) or made[-1])
+    a, s = torch.ones((4096, 4096), device=dev()), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            a @ a                                                       # milliseconds
+    y = torch.empty_like(q["r"])
+    s.wait_stream(torch.cuda.current_stream())
+    bbs.nvfp4_moe_gemv(0, q["x"], q["ids"], q["w"], 16, *q["W"], y, 1, act=bbs.ACT_GELU, residual=q["r"], stream=s)
+    size, at = made[0].numel(), made.pop().data_ptr()
+    other = torch.empty((size,), dtype=torch.uint8, device=dev())
+    busy = not s.query()
+    assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert busy and torch.equal(y, eager[0])
