@@ -174,7 +174,7 @@ class QLinearBiasActFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, b, r, act, seed, step, signs, grad=True):
         lead, K, N = x.shape[:-1], x.shape[-1], w.shape[0]
-        x2 = _bits(x.reshape(-1, K))
+        x2 = _aligned(_bits(x.reshape(-1, K)))
         M, dev = x2.shape[0], x.device
         ws = amax_workspace(dev)
         need_x, need_w, need_b, need_r = (grad and n for n in ctx.needs_input_grad[:4])
@@ -205,7 +205,7 @@ class QLinearBiasActFn(torch.autograd.Function):
         dx = dw = db = None
         dr = dy.to(r_dtype) if need_r else None
         if need_x or need_w or need_b:
-            g = _bits(dy.reshape(M, N))
+            g = _aligned(_bits(dy.reshape(M, N)))
             z8 = MXFP8Tensor(t[6], t[7], M, N) if act != ACT_NONE else None
             dz = torch.empty_like(g) if z8 and (need_x or need_w) else None
             if need_b:
@@ -300,7 +300,7 @@ class QLinearInference:
         _check_residual(residual, x.shape[:-1], N)
         _on_current(None, x, self.weight.codes, *(() if residual is None else (residual,)))
         lead = x.shape[:-1]
-        x2 = x.reshape(-1, K).to(torch.bfloat16).contiguous()
+        x2 = _aligned(x.reshape(-1, K).to(torch.bfloat16).contiguous())
         T, dev = x2.shape[0], x.device
         r = _residual(residual, T, N)
         y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
@@ -495,7 +495,7 @@ class QMoEInference:
     F], and w_gate [E, F, K] for gated experts (None: plain ones, act may then be
     None).  The call takes the router's choice: ids [..., k] (integers; outside
     [0, E): no expert) and weights [..., k] (None: 1), and an optional residual
-    [..., N].  GEMV_MAX_TOKENS tokens go through the two kernels at a time (many more
+    [..., N].  GEMV_MAX_TOKENS tokens go through the kernels at a time (many more
     tokens read the experts' weights again for each group of them)."""
 
     def __init__(self, w_gate, w_up, w_down, act="silu"):
@@ -522,7 +522,7 @@ class QMoEInference:
             raise ValueError("ids must be integers")
         _check_residual(residual, lead, N)
         _on_current(None, x, ids, self.up.codes, *(t for t in (weights, residual) if t is not None))
-        x2 = x.reshape(-1, K).to(torch.bfloat16).contiguous()
+        x2 = _aligned(x.reshape(-1, K).to(torch.bfloat16).contiguous())
         T, k = x2.shape[0], ids.shape[-1]
         # what does not fit 32 bits is no expert's number
         ids = ids.reshape(T, k)

@@ -273,3 +273,33 @@ def test_refusals(L):
                 lambda: m.inference()(x.cpu()), lambda: m.inference()(x, x)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_inputs_at_any_address(L):
+    """Contiguous inputs and gradients that begin between two 16-byte addresses."""
+    announce("layers: inputs at any address")
+
+    def moved(t):
+        flat = torch.empty((t.numel() + 1,), dtype=t.dtype, device=t.device)
+        flat[1:] = t.detach().reshape(-1)
+        return flat[1:].view(t.shape)
+
+    m, x, r, dy, _ = make(L, 64, 96, 160, "gelu", True)
+    want = m(x, r)
+    want.backward(dy)
+    grads = [t.grad.clone() for t in (x, r, m.weight, m.bias)]
+    m.weight.grad = m.bias.grad = None
+    m.step = 0
+    x2, r2 = moved(x).requires_grad_(True), moved(r).requires_grad_(True)
+    y = m(x2, r2)
+    y.backward(moved(dy))
+    assert torch.equal(y, want)
+    assert all(torch.equal(a, b.grad) for a, b in zip(grads, (x2, r2, m.weight, m.bias)))
+    q = m.inference()
+    for T in (5, 64 * 2):
+        v = normal((T, 96), torch.bfloat16, 7)
+        assert torch.equal(q(v), q(moved(v)))
+    W = [normal((4, a, b), torch.bfloat16, 8) for a, b in ((64, 96), (64, 96), (32, 64))]
+    e = L.QMoEInference(*W)
+    v, ids = normal((70, 96), torch.bfloat16, 9), torch.arange(140, device=dev()).reshape(70, 2) % 4
+    assert torch.equal(e(v, ids), e(moved(v), ids))
