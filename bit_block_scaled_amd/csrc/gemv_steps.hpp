@@ -72,6 +72,7 @@ struct Place {
 
 template <int SC, int R>
 __device__ __forceinline__ Place<R> place_of(const GemvParams &p, int64_t n0) {
+    static_assert(4 * R <= 16, "NVFP4 rows are a multiple of 16, and a tile's scale serves 16 rows");
     Place<R> pl;
     const int lane = threadIdx.x & 63, i = lane & 3, b = lane >> 2;
 #pragma unroll

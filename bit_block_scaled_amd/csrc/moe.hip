@@ -16,8 +16,8 @@
 //     the experts' weights through registers, a kernel for each projection, and a
 //     third kernel adds up the experts' outputs.
 // Measured, replayed from a graph (codes and scales at TB/s in brackets): 1 token,
-// 8 of 64 plain experts, 50 MB: 17.7 us (2.9); 1 token, 2 of 8 gated, 177 MB: 45.9 us
-// (3.9); 16 tokens, MXFP4, 430 MB: 112 us (3.8); 64 tokens, 8 of 64, NVFP4, 61 experts
+// 8 of 64 plain experts, 50 MB: 17.7 us (2.9); 1 token, 2 of 8 gated, 177 MB: 41.0 us
+// (4.3); 16 tokens, MXFP4, 430 MB: 112 us (3.8); 64 tokens, 8 of 64, NVFP4, 61 experts
 // chosen, 582 MB: 184 us (3.2).
 //
 // The hidden values go between the kernels as two BF16 parts (three for FP32
@@ -1037,11 +1037,25 @@ hipError_t launch_stream(const MoeParams &p, const MoeShape &sh, hipStream_t s) 
     return hipGetLastError();
 }
 
+// With gated NVFP4 experts one wave takes all of K, and 16 rows, where that leaves every
+// CU six waves: a wave then loads twice as much a step, and joins nothing in LDS.
+// Measured (against two waves of half the rows): 2 of 8 experts, 1 token, 1792 waves, 41.0
+// us and 45.8, 4 tokens 121 and 147; 8 of 64, 2 tokens, 1536 waves, 36.8 and 40.0, 4
+// tokens 58.7 and 67.6, but 1 token, 768 waves, 26.9 and 23.6.  MXFP4, 16 of 64 experts
+// with 1536 waves, 48.3 and 44.7.
 template <int SC, int NM, int TT>
 hipError_t up_few(const MoeParams &p, hipStream_t s) {
-    constexpr int R = 4 / NM;
-    const dim3 grid((unsigned)((p.F + 4 * R - 1) / (4 * R)), (unsigned)moe_slots(p.T, p.k, p.E));
-    hipLaunchKernelGGL((moe_up_few_kernel<SC, NM, TT, R>), grid, dim3(64 * kUpFewSplit), 0, s, p);
+    const int64_t slots = moe_slots(p.T, p.k, p.E);
+    constexpr int R = 4 / NM, RW = 4;
+    auto blocks = [&](int r) { return (unsigned)((p.F + 4 * r - 1) / (4 * r)); };
+    if constexpr (SC != kRows32 && NM == 2) {
+        if (blocks(RW) * slots >= 6 * device_cus(s)) {
+            hipLaunchKernelGGL((moe_up_few_kernel<SC, NM, TT, RW>), dim3(blocks(RW), (unsigned)slots), dim3(64), 0, s, p);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((moe_up_few_kernel<SC, NM, TT, R>), dim3(blocks(R), (unsigned)slots), dim3(64 * kUpFewSplit), 0, s,
+                       p);
     return hipGetLastError();
 }
 

@@ -120,6 +120,11 @@ CASES = [
     (64, 1024, 32, 32, 32, 16, "mxfp4", False, False, "gelu", True, True, "bf16", "", 0),
     (64, 10, 4, 1024, 640, 32, "nvfp4", False, False, "silu", True, True, "bf16", "one", 0),
     (40, 16, 4, 64, 64, 64, "nvfp4", True, True, "silu", True, True, "f32", "none", 8),
+    # up to four tokens, hidden rows and experts enough for whole rows a wave
+    (1, 12, 6, 4112, 528, 32, "nvfp4", False, True, "silu", True, True, "bf16", "", 0),
+    (2, 40, 8, 3200, 272, 48, "nvfp4", True, False, "gelu", True, False, "f32", "dropped", 8),
+    (3, 64, 16, 592, 1552, 64, "nvfp4", False, True, "gelu", False, True, "f32", "twice", 0),
+    (4, 10, 4, 5216, 784, 80, "nvfp4", True, True, "silu", True, True, "bf16", "", 8),
     # five tokens on, with weights enough for the streaming kernels
     (5, 64, 8, 544, 1568, 1040, "nvfp4", False, False, "silu", True, False, "bf16", "", 0),
     (8, 64, 8, 528, 1552, 1040, "nvfp4", False, True, "gelu", True, True, "f32", "", 8),
