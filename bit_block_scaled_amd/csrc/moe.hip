@@ -4,7 +4,7 @@
 //
 // The chosen experts' weights bound the layer: each is read once, against 2 flops
 // a weight and token.  Three forms, by the launch rules at the end:
-//   - up to four tokens, two kernels with 4 x 4 x 4 products.  The first kernel's
+//   - a few tokens, two kernels with 4 x 4 x 4 products.  The first kernel's
 //     workgroups take one expert and a few of its hidden rows; they find the expert's
 //     tokens themselves by looking through the ids (T k of them), so nothing has to be
 //     sorted first.  The second kernel's workgroups take a few output columns of all
@@ -153,7 +153,7 @@ constexpr int kSplit = 8;              // waves of a workgroup
 constexpr int kUpFewSplit = 2;
 
 // ---------------------------------------------------------------------------
-// Up projections, up to four tokens at a time (4 x 4 x 4 products).
+// Up projections, four tokens at a time (4 x 4 x 4 products).
 // ---------------------------------------------------------------------------
 template <int SC, int NM, int TT, int R>
 __global__ __launch_bounds__(64 * kUpFewSplit) void moe_up_few_kernel(MoeParams p) {
@@ -1019,6 +1019,19 @@ bool streams(const MoeParams &p) {
            moe_up_shape(p.T, p.k, p.K).rows > 0;
 }
 
+// The 4 x 4 x 4 products leave no rows empty at a few tokens, but expand a code again for
+// every four of an expert.  NVFP4, up to eight tokens, against the other two forms: 8 of
+// 64 experts, 5 tokens 71.5 us and 85.9, 8 tokens 94.7 and 102; 2 of 8, 6 tokens 130 and
+// 142, 8 tokens 154 and 152; 2 of 16 small ones, 8 tokens 15.3 and 17.2 (16 tokens and 8 of 64:
+// 198 and 135).  MXFP4 streams sooner, as its codes are cheap to expand: 2 of 8, 3 tokens
+// 103 and 85.8, 4 tokens 138 and 119; but below the streaming kernels' size 4 tokens 25.0 and
+// 30.3, 5 tokens 20.7 and 17.5.
+template <int SC>
+bool few_tokens(const MoeParams &p) {
+    if (SC != kRows32) return p.T <= 8;
+    return p.T <= 2 || (p.T <= 4 && !streams(p));
+}
+
 // Steps in flight beside the one in use: two for NVFP4 (64 tokens, 118 us against 123
 // with one), one for MXFP4, whose steps are short (16 tokens, 65 us against 68 with two).
 template <int SC>
@@ -1063,7 +1076,7 @@ template <int SC, int NM>
 hipError_t up(const MoeParams &p, hipStream_t s) {
     if (p.T == 1) return up_few<SC, NM, 1>(p, s);
     if (p.T == 2) return up_few<SC, NM, 2>(p, s);
-    if (p.T <= 4) return up_few<SC, NM, 4>(p, s);
+    if (few_tokens<SC>(p)) return up_few<SC, NM, 4>(p, s);
     if (streams(p))
         return launch_stream<moe_stream_kernel<SC, NM, 2 / NM, 0, 1, kRing<SC>>>(p, moe_up_shape(p.T, p.k, p.K), s);
     const dim3 grid((unsigned)((p.F + 15) / 16), (unsigned)moe_slots(p.T, p.k, p.E));
@@ -1074,8 +1087,9 @@ hipError_t up(const MoeParams &p, hipStream_t s) {
 template <int SC, int NP>
 hipError_t down_stream(const MoeParams &p, hipStream_t s) {
     const MoeShape sh = moe_down_shape(p.T, p.k, p.F);
-    const hipError_t e = sh.rows == 32 ? launch_stream<moe_stream_kernel<SC, 1, 2, NP, 2, kRing<SC>>>(p, sh, s)
-                                       : launch_stream<moe_stream_kernel<SC, 1, 2, NP, 1, kRing<SC>>>(p, sh, s);
+    hipError_t e;
+    if (SC == kRows32 && sh.rows == 16) e = launch_stream<moe_stream_kernel<kRows32, 1, 2, NP, 1, kRing<kRows32>>>(p, sh, s);
+    else e = launch_stream<moe_stream_kernel<SC, 1, 2, NP, 2, kRing<SC>>>(p, sh, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(moe_sum_kernel, dim3((unsigned)((p.N + 63) / 64), (unsigned)p.T), dim3(64), 0, s, p, sh.ranges);
     return hipGetLastError();
@@ -1083,7 +1097,7 @@ hipError_t down_stream(const MoeParams &p, hipStream_t s) {
 
 template <int SC>
 hipError_t down(const MoeParams &p, hipStream_t s) {
-    if (p.T <= 4) {
+    if (few_tokens<SC>(p)) {
         if (!p.bf16_out) return launch_down<moe_down_few_kernel<SC, 3, 1, 4>>(p, 16, 0, s);
         if (p.T == 1) return launch_down<moe_down_few_kernel<SC, 2, 1, 4>>(p, 16, 0, s);
         return launch_down<moe_down_few_kernel<SC, 2, 2, 4>>(p, 16, 0, s);

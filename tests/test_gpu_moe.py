@@ -120,14 +120,18 @@ CASES = [
     (64, 1024, 32, 32, 32, 16, "mxfp4", False, False, "gelu", True, True, "bf16", "", 0),
     (64, 10, 4, 1024, 640, 32, "nvfp4", False, False, "silu", True, True, "bf16", "one", 0),
     (40, 16, 4, 64, 64, 64, "nvfp4", True, True, "silu", True, True, "f32", "none", 8),
-    # up to four tokens, hidden rows and experts enough for whole rows a wave
+    # a few tokens, hidden rows and experts enough for whole rows a wave
     (1, 12, 6, 4112, 528, 32, "nvfp4", False, True, "silu", True, True, "bf16", "", 0),
     (2, 40, 8, 3200, 272, 48, "nvfp4", True, False, "gelu", True, False, "f32", "dropped", 8),
     (3, 64, 16, 592, 1552, 64, "nvfp4", False, True, "gelu", False, True, "f32", "twice", 0),
     (4, 10, 4, 5216, 784, 80, "nvfp4", True, True, "silu", True, True, "bf16", "", 8),
-    # five tokens on, with weights enough for the streaming kernels
+    # three tokens on (MXFP4; NVFP4: nine), with weights enough for the streaming kernels
     (5, 64, 8, 544, 1568, 1040, "nvfp4", False, False, "silu", True, False, "bf16", "", 0),
     (8, 64, 8, 528, 1552, 1040, "nvfp4", False, True, "gelu", True, True, "f32", "", 8),
+    (3, 8, 2, 2080, 2720, 2720, "mxfp4", False, True, "silu", True, True, "bf16", "", 0),
+    (4, 16, 3, 2080, 2080, 2080, "mxfp4", False, True, "gelu", True, True, "f32", "dropped", 8),
+    (8, 64, 8, 544, 1568, 1040, "mxfp4", False, True, "silu", True, False, "bf16", "", 0),
+    (9, 64, 8, 528, 1552, 1040, "nvfp4", False, True, "silu", True, False, "bf16", "twice", 0),
     (9, 100, 12, 544, 608, 1568, "mxfp4", False, True, "gelu", True, True, "f32", "dropped", 8),
     (24, 6, 3, 2064, 4624, 2080, "nvfp4", True, True, "silu", True, True, "f32", "", 0),
     (13, 8, 2, 5136, 1040, 2064, "nvfp4", False, True, "silu", True, False, "bf16", "", 0),
@@ -236,7 +240,7 @@ def run(bbs, q, stream=None):
     return y, z
 
 
-@pytest.mark.parametrize("T,wide", [(1, 1), (3, 1), (20, 1), (20, 10)])
+@pytest.mark.parametrize("T,wide", [(1, 1), (3, 1), (3, 10), (20, 1), (20, 10)])
 def test_streams_and_graphs(bbs, T, wide):
     """On a side stream, and captured and replayed with new tokens and another
     routing, with eager calls between the replays."""
@@ -278,12 +282,12 @@ def test_calls_at_once(bbs, wide):
     assert same(alone[0], both[0]) and same(alone[1], both[1])
 
 
-@pytest.mark.parametrize("wide", [1, 10])
-def test_two_graphs_of_one_workspace(bbs, wide):
+@pytest.mark.parametrize("T,wide", [(5, 1), (20, 1), (20, 10)])
+def test_two_graphs_of_one_workspace(bbs, T, wide):
     """Two captured calls that share a workspace, replayed in turn on one stream."""
     announce("moe: two graphs, one workspace")
-    a, b = problem(bbs, 5, 1, wide), problem(bbs, 5, 30, wide)
-    ws = bbs.moe_workspace(5, 4, 16, 208 * wide, 160 * wide, dev())
+    a, b = problem(bbs, T, 1, wide), problem(bbs, T, 30, wide)
+    ws = bbs.moe_workspace(T, 4, 16, 208 * wide, 160 * wide, dev())
 
     def call(q):
         y = torch.empty_like(q["r"])
