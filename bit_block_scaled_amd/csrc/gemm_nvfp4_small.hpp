@@ -77,6 +77,38 @@ __device__ __forceinline__ void join_groups(uint8_t *smem, int grp, int wave, in
     }
 }
 
+// As join_groups for two column blocks of NV values each, of which group 0 receives the
+// first one's sums and group 1 the second one's, in v (a: the group's shares of both).
+// The same additions in the same order.
+template <int G, int NV>
+__device__ __forceinline__ void join_blocks(uint8_t *smem, int grp, int wave, int lane, const float (&a)[2][NV],
+                                            float (&v)[NV]) {
+    __syncthreads();                               // the rings are free
+    // block j's shares, of the G - 1 groups that do not own it
+    float *const part = reinterpret_cast<float *>(smem) + (wave * NV) * 64 + lane;
+    auto at = [&](int j, int g, int i) -> float & { return part[((j * (G - 1) + (g < j ? g : g - 1)) * 4 * NV + i) * 64]; };
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (grp != j) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) at(j, grp, i) = a[j][i];
+        }
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = a[0][i] + at(0, 1, i);
+    } else if (grp == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = at(1, 0, i) + a[1][i];
+    }
+    if (grp < 2) {
+#pragma unroll
+        for (int g = 2; g < G; ++g)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[i] += at(grp, g, i);
+    }
+}
+
 template <int TM>
 struct Stage {
     uint8_t a[TM * 64];              // 64 code bytes a row and slab, swizzled as big::Stage
@@ -126,7 +158,10 @@ struct GatedSide {
 // (blockDim.x = 256 G, LDS of G NS stages at smem).
 // finish(p, acc, m, n0, wn, lane) receives the FP32 sums, without decode scales: in
 // acc[i][j] a lane holds row m + 32 i + lane % 32 and, of the tile's 32-column
-// block 2 wn + j of B's rows, 16 consecutive columns (column above).
+// block 2 wn + j of B's rows, 16 consecutive columns (column above).  With one operand
+// it is finish(p, v, m, n, lane) for a column block at a time: in v[i] a lane holds row
+// m + 32 i + lane % 32 and 16 columns from n + 16 (lane / 32) on.  Two groups then finish a
+// block each.
 template <int TM, int NS, int G, typename Side, typename Params, typename Finish>
 __device__ __forceinline__ void run_tile(uint8_t *smem, const Params &p, Finish finish) {
     constexpr int RA = TM / 64;                    // 32-row blocks of a wave
@@ -308,9 +343,26 @@ __device__ __forceinline__ void run_tile(uint8_t *smem, const Params &p, Finish 
         }
     }
 
-    join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[RA * 32]>(acc));
-    if (grp) return;
-    finish(p, acc, m0 + wm * (TM / 2), n0, wn, lane);
+    if constexpr (Side::kMats == 2) {
+        join_groups<G>(smem, grp, wave, lane, reinterpret_cast<float(&)[RA * 32]>(acc));
+        if (grp) return;
+        finish(p, acc, m0 + wm * (TM / 2), n0, wn, lane);
+    } else {
+        f32x16 v[2][RA];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < RA; ++i) v[j][i] = acc[i][j];
+        if constexpr (G == 1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) finish(p, v[j], m0 + wm * (TM / 2), n0 + wn * 64 + j * 32, lane);
+        } else {
+            f32x16 o[RA];
+            join_blocks<G>(smem, grp, wave, lane, reinterpret_cast<const float(&)[2][RA * 16]>(v),
+                           reinterpret_cast<float(&)[RA * 16]>(o));
+            if (grp < 2) finish(p, o, m0 + wm * (TM / 2), n0 + wn * 64 + grp * 32, lane);
+        }
+    }
 }
 
 // Launch with dynamic LDS; the kernel's limit is raised once per kernel.

@@ -18,61 +18,80 @@ using small::launch, small::run_tile, small::tiles_of;
 using small::PlainSide;
 
 // ---------------------------------------------------------------------------
-// Forward: TM rows by 128 columns.
+// Forward: TM rows by 128 columns.  The epilogue of a 32 x 32 block loads all it
+// needs before its first store: loads and stores share one counter, so a load behind a
+// store would wait for it.  Where groups of waves split K, two of them finish a column
+// block each.  Measured with GELU, bias and residual, replayed from a graph: 528 x 2736 x
+// 1552, FP32, 16.6 us (loads between the stores, one group finishing: 19.4), 256 x 4096
+// x 1536 14.8 (16.9), 2048 x 4096 x 1552, BF16, 41.5 (46.8).  64 x 512 x 512 takes 8.5: launch,
+// first copies, join and epilogue; beyond that a slab costs 0.7 us on a CU, 45% of it
+// the expansion.
 // ---------------------------------------------------------------------------
+// Sixteen consecutive values of a bias or a residual, as loaded.
+struct Raw16 {
+    uint4 v[4];
+};
+
+__device__ __forceinline__ void load16(Raw16 &o, const void *p, int bf16, int64_t at) {
+    const uint4 *const from = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + at * (bf16 ? 2 : 4));
+    o.v[0] = from[0];
+    o.v[1] = from[1];
+    if (!bf16) {
+        o.v[2] = from[2];
+        o.v[3] = from[3];
+    }
+}
+
+__device__ __forceinline__ void add16(f32x16 &v, const Raw16 &o, int bf16) {
+    if (bf16) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t w = big::word(o.v[e >> 2], e & 3);
+            v[2 * e] += __uint_as_float(w << 16);
+            v[2 * e + 1] += __uint_as_float(w & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] += __uint_as_float(big::word(o.v[e >> 2], e & 3));
+    }
+}
+
 template <int TM, int NS, int G, bool BF16_OUT>
 __global__ __launch_bounds__(kThreads * G, TM == 256 ? 2 : 1) void linear_kernel(LinearParams p) {
     constexpr int RA = TM / 64;                    // 32-row blocks of a wave
     extern __shared__ __align__(16) uint8_t smem[];
-    auto finish = [](const LinearParams &p, const f32x16 (&acc)[RA][2], int64_t mw, int64_t n0, int wn, int lane)
+    auto finish = [](const LinearParams &p, const f32x16 (&acc)[RA], int64_t mw, int64_t nb, int lane)
                       __attribute__((always_inline)) {
         const int h = lane >> 5, rl = lane & 31;
         const float sb = p.b.s_dec[0];
+        const int64_t n = nb + 16 * h, nc = n < p.N ? n : 0;        // the lane's first column
+        Raw16 bias, res;
+        if (p.bias) load16(bias, p.bias, p.bias_bf16, nc);
 #pragma unroll
         for (int i = 0; i < RA; ++i) {
-            const int64_t m = mw + i * 32 + rl;
-            const float scale = p.a.s_dec[p.a.sdec_rows ? (m < p.M ? m : p.M - 1) : 0] * sb;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t n = n0 + wn * 64 + j * 32 + 16 * h;   // the lane's first column
-                const bool in = m < p.M && n < p.N;
-                f32x16 v = acc[i][j];
-                scale16(v, scale);
-                if (p.bias) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float b[4];
-                        load_bias4(p.bias, p.bias_bf16, n < p.N ? n + 4 * q : 0, b);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[4 * q + e] = v[4 * q + e] + b[e];
-                    }
+            const int64_t m = mw + i * 32 + rl, mc = min(m, p.M - 1);
+            const bool in = m < p.M && n < p.N;
+            const float scale = p.a.s_dec[p.a.sdec_rows ? mc : 0] * sb;
+            if (p.r) load16(res, p.r, BF16_OUT, mc * p.ldr + nc);
+            f32x16 v = acc[i];
+            scale16(v, scale);
+            if (p.bias) add16(v, bias, p.bias_bf16);
+            if (p.z_codes) {
+                uint32_t w[4];
+                const uint32_t byte = checkpoint16(v, w);
+                if (in) {
+                    *reinterpret_cast<uint4 *>(p.z_codes + m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (h == 0) p.z_scales[m * (p.N / 32) + n / 32] = (uint8_t)byte;
                 }
-                if (p.z_codes) {
-                    uint32_t w[4];
-                    const uint32_t byte = checkpoint16(v, w);
-                    if (in) {
-                        *reinterpret_cast<uint4 *>(p.z_codes + m * p.N + n) = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (h == 0) p.z_scales[m * (p.N / 32) + n / 32] = (uint8_t)byte;
-                    }
-                }
-                if (!in) continue;
-                act_all<BF16_OUT, 16>(v, p.act);
-                if (p.r) {
-                    const int64_t at = m * p.ldr + n;
+            }
+            if (!in) continue;
+            act_all<BF16_OUT, 16>(v, p.act);
+            if (p.r) add16(v, res, BF16_OUT);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float r[4];
-                        load_bias4(p.r, BF16_OUT, at + 4 * q, r);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[4 * q + e] = v[4 * q + e] + r[e];
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const float y0[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-                    const float y1[4] = {v[4 * q + 4], v[4 * q + 5], v[4 * q + 6], v[4 * q + 7]};
-                    store8<BF16_OUT>(p.c, m * p.ldc + n + 4 * q, y0, y1);
-                }
+            for (int q = 0; q < 4; q += 2) {
+                const float y0[4] = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+                const float y1[4] = {v[4 * q + 4], v[4 * q + 5], v[4 * q + 6], v[4 * q + 7]};
+                store8<BF16_OUT>(p.c, m * p.ldc + n + 4 * q, y0, y1);
             }
         }
     };

@@ -448,7 +448,7 @@ int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t 
                         int64_t ldr, void *y, int32_t y_dtype, int64_t ldy, void *stream);
 
 /* A whole mixture-of-experts layer for 1 to BBS_GEMV_MAX_TOKENS tokens, in two
- * kernels:
+ * or three kernels:
  *   y[t] = residual[t] + sum over j < k of weights[t, j] * expert_e(x[t]),  e = ids[t, j],
  *   expert_e(x) = (act(x * Wg_e^T) * (x * Wu_e^T)) * Wd_e^T,   gated (Wg given), or
  *   expert_e(x) = act(x * Wu_e^T) * Wd_e^T                     plain (Wg NULL).
@@ -459,11 +459,11 @@ int nvfp4_gemv_bias_act(int32_t fmt, const uint16_t *x, int64_t tokens, int64_t 
  * dropped slot and adds nothing (a token without experts gets its residual, or
  * +0); an expert chosen twice by a token counts twice.  weights is tokens x k FP32, or
  * NULL (1).  act is SiLU or GELU, for plain experts also BBS_ACT_NONE.
- * residual (or NULL) is tokens x N of y_dtype with row stride ldr, and may be y.
- * Everything is computed in FP32 and rounded once to y_dtype, except that the
+ * residual (or NULL) is tokens x N of y_dtype with row stride ldr, and may be y with
+ * ldr == ldy.  Everything is computed in FP32 and rounded once to y_dtype, except that the
  * hidden values are held in two BF16 parts (16 significant bits) for BF16 outputs
  * and in three (24) for FP32 ones; they must be below 2^127.  The sums' order
- * depends on sizes, format and routing alone; a token's answer then differs from
+ * depends on sizes, format, routing and the device's number of CUs alone; a token's answer then differs from
  * what it gets beside other tokens by the rounding of FP32 sums.
  * ws: nvfp4_moe_ws_bytes(tokens, k, experts, F, N) bytes of device workspace, 16-byte
  * aligned, not kept; calls that overlap in time need one each.
