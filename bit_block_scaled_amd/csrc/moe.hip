@@ -148,8 +148,9 @@ __device__ __forceinline__ void finish_hidden(const MoeParams &p, const GemvPara
 }
 
 constexpr int kSplit = 8;              // waves of a workgroup
-// Of moe_up_few_kernel, whose workgroups are many (hidden rows x experts): 2 of 8
-// experts, 1 token, 30.1 us against 32.5 with four and 35 with eight.
+// Of moe_up_few_kernel with 16 / NM rows a workgroup: 2 of 8 experts, 1 token, 30.1 us
+// against 32.5 with four waves and 35 with eight; 8 of 64, 9.0 against 11.0 with one (where
+// one wave is better, see up_few).
 constexpr int kUpFewSplit = 2;
 
 // ---------------------------------------------------------------------------
