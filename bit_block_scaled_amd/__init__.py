@@ -400,9 +400,19 @@ def _on_current(stream, *tensors):
     return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
+def _workspace(make, stream):
+    """make()'s workspace of this call alone, from the pool of the stream that the call runs
+    on (None: the current one).  The allocator orders a block's owners on its own stream only:
+    one from another pool may still be in use there by work that `stream` does not wait for."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
 def _used_on(ws, stream):
-    """A workspace of this call alone, kept from reuse until the stream is past the call: the
-    allocator knows it as the current stream's."""
+    """Keeps a workspace from reuse until `stream` is past the call, also if its maker took it
+    from another stream's pool (for a block of the stream's own this changes nothing)."""
     if stream is not None:
         ws.record_stream(stream)
 
@@ -533,7 +543,7 @@ def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=Non
     checkpoint of z: dZ = dY * act'(z) and dbias = its sum over the rows.  dY and dZ:
     BF16 patterns [M, N] (dZ may be dY); dbias: [N] float32 or bfloat16; z_ckpt is
     not read, and may be None, with ACT_NONE.  ws: BIAS_PARTS * N float32 of
-    workspace for dbias (allocated if None)."""
+    workspace for dbias (allocated on the call's stream if None)."""
     M, N = dY.shape
     ldy = _output_ld(dY, OUT_BF16, M, N, None, "dY")
     ldz = _output_ld(dZ, OUT_BF16, M, N, None, "dZ") if dZ is not None else 0
@@ -545,7 +555,7 @@ def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=Non
     own = dbias is not None and ws is None
     if dbias is not None:
         if own:
-            ws = torch.empty((BIAS_PARTS * N,), dtype=torch.float32, device=dY.device)
+            ws = _workspace(lambda: torch.empty((BIAS_PARTS * N,), dtype=torch.float32, device=dY.device), stream)
         elif ws.dtype != torch.float32 or not ws.is_contiguous() or ws.numel() < BIAS_PARTS * N:
             raise ValueError(f"ws must hold {BIAS_PARTS * N} adjacent float32 values")
     more = [t for t in (dZ, dbias, ws) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
@@ -590,7 +600,7 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
     x BF16 patterns [T, K]; ids int32 [T, k] (entries outside [0, experts) add
     nothing), weights float32 [T, k] or None (1); weights in the format fmt (NVFP4
     with one decode scale an expert); residual [T, N] of y's type, y itself allowed;
-    ws: moe_workspace(...), allocated if None."""
+    ws: moe_workspace(...), allocated on the call's stream if None."""
     if not 1 <= experts <= MOE_MAX_EXPERTS:
         raise ValueError(f"experts must be in [1, {MOE_MAX_EXPERTS}]")
     T, cols = x.shape
@@ -620,7 +630,7 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
         ldx = K                          # a single row's stride may be anything in PyTorch
     own = ws is None
     if own:
-        ws = moe_workspace(T, k, experts, F, N, x.device)
+        ws = _workspace(lambda: moe_workspace(T, k, experts, F, N, x.device), stream)
     elif ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < lib.nvfp4_moe_ws_bytes(T, k, experts, F, N):
         raise ValueError("ws must be a moe_workspace of the call's sizes")
     s = _on_current(stream, ws, *tensors)

@@ -348,3 +348,41 @@ def test_own_workspace_on_another_stream(bbs, monkeypatch):
     assert other.data_ptr() != at
     torch.cuda.synchronize()
     assert busy and torch.equal(y, eager[0])
+
+
+@pytest.mark.parametrize("op", ["moe", "bias"])
+def test_own_workspace_leaves_pending_work_alone(bbs, monkeypatch, op):
+    """A workspace the call allocates for a given stream is no block that work on the
+    current stream, which the given one does not wait for, still uses."""
+    announce(f"{op}: own workspace, other stream, pending work on the current one")
+    q = problem(bbs, 20, 1)
+    dy, db = normal((2048, 512), torch.bfloat16, 1), torch.empty((512,), device=dev())
+    ys = torch.empty_like(q["r"]), torch.empty_like(q["r"])
+
+    def call(i, stream=None):
+        if op == "moe":
+            bbs.nvfp4_moe_gemv(0, q["x"], q["ids"], q["w"], 16, *q["W"], ys[i], 1, residual=q["r"], stream=stream)
+            return ys[i]
+        bbs.mxfp8_bias_act_bwd(dy, None, bbs.ACT_NONE, None, db, stream=stream)
+        return db
+
+    want = call(0).clone()
+    size = bbs.moe_workspace(20, 4, 16, 208, 160).numel() if op == "moe" else bbs.BIAS_PARTS * 512 * 4
+    made, keep = [], bbs._used_on
+    monkeypatch.setattr(bbs, "_used_on", lambda ws, stream: made.append(ws.data_ptr()) or keep(ws, stream))
+    a, s = torch.ones((4096, 4096), device=dev()), torch.cuda.Stream()
+    call(1, s)                                                          # the stream's pool has memory
+    torch.cuda.synchronize()
+    for _ in range(40):
+        a @ a                                                           # milliseconds, on the current stream
+    used = torch.empty((size,), dtype=torch.uint8, device=dev())
+    used.fill_(7)
+    sums, at = used.view(-1, 256).sum(1), used.data_ptr()               # read after the call below has run
+    del used
+    got = call(1, s)
+    busy = not torch.cuda.current_stream().query()
+    s.synchronize()
+    assert made[-1] != at and busy
+    assert torch.equal(got, want)
+    torch.cuda.synchronize()
+    assert bool((sums == 7 * 256).all())
