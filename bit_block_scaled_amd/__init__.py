@@ -236,6 +236,16 @@ def amax_workspace(device="cuda"):
     return torch.empty((AMAX_WS_FLOATS,), dtype=torch.float32, device=device)
 
 
+def _workspace(make, stream):
+    """make()'s workspace of this call alone, from the pool of the stream that the call runs
+    on (None: the current one).  The allocator orders a block's owners on its own stream only:
+    one from another pool may still be in use there by work that `stream` does not wait for."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
 # ---------------------------------------------------------------------------
 # Entry points
 # ---------------------------------------------------------------------------
@@ -248,12 +258,13 @@ def nvfp4_quantize(x, row=None, col=None, row_mx8=None, *, row_round=RTN, row_rn
     (row stride x.stride(0)).  row / col: NVFP4Tensor outputs; row_mx8: MXFP8Tensor.
     row_per_token / row_four_six: activation options of the row copy (a
     per-token row copy needs NVFP4Tensor.empty(..., sdec_per_row=True)).
-    gelu: the row / row_mx8 copies are of GELU(x) (tanh form, FP32)."""
+    gelu: the row / row_mx8 copies are of GELU(x) (tanh form, FP32).
+    amax_ws: amax_workspace(), allocated on the call's stream if None."""
     rd = row.desc() if row is not None else None
     cd = col.desc() if col is not None else None
     md = row_mx8.desc() if row_mx8 is not None else None
     if amax_ws is None:
-        amax_ws = amax_workspace(x.device)
+        amax_ws = _workspace(lambda: amax_workspace(x.device), stream)
     a = QuantArgs(_ptr(x), x.shape[0], x.shape[1], x.stride(0),
                   C.pointer(rd) if rd else None, row_round, Rng(*row_rng),
                   C.pointer(cd) if cd else None, col_round, Rng(*col_rng),
@@ -334,7 +345,7 @@ def nvfp4_gemm_quant(A, B, s_enc, Y, gelu=False, amax=None, ws=None, stream=None
     (optional one-element float32 device tensor) receives max |y|."""
     ad, bd, yd = A.desc(), B.desc(), Y.desc()
     if gelu and ws is None:
-        ws = amax_workspace(s_enc.device)
+        ws = _workspace(lambda: amax_workspace(s_enc.device), stream)
     _check(lib.nvfp4_gemm_quant(C.byref(ad), C.byref(bd), _ptr(s_enc), int(gelu), C.byref(yd),
                                 _ptr(amax), _ptr(ws), _stream(stream)))
 
@@ -343,7 +354,7 @@ def grouped_nvfp4_gemm_quant(A, row_index, group_offsets, G, max_rows, B, N, s_e
                              gelu=False, amax=None, ws=None, stream=None):
     ad, bd, yd = A.desc(), B.desc(), Y.desc()
     if gelu and ws is None:
-        ws = amax_workspace(s_enc.device)
+        ws = _workspace(lambda: amax_workspace(s_enc.device), stream)
     _check(lib.grouped_nvfp4_gemm_quant(C.byref(ad), _ptr(row_index), _ptr(group_offsets), G,
                                         max_rows, C.byref(bd), N, _ptr(s_enc), int(gelu),
                                         C.byref(yd), _ptr(amax), _ptr(ws), _stream(stream)))
@@ -398,16 +409,6 @@ def _on_current(stream, *tensors):
     if dev < 0 or dev != _device() or (stream is not None and stream.device_index != dev):
         raise ValueError("the tensors and the stream must be on the current GPU")
     return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _workspace(make, stream):
-    """make()'s workspace of this call alone, from the pool of the stream that the call runs
-    on (None: the current one).  The allocator orders a block's owners on its own stream only:
-    one from another pool may still be in use there by work that `stream` does not wait for."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        return make()
 
 
 def _used_on(ws, stream):

@@ -35,7 +35,7 @@ def made(monkeypatch):
 
     def entry(name, at):
         def call(*a):
-            ws = a[at]
+            ws = a[0]._obj.amax_ws if name == "nvfp4_quantize" else a[at]
             seen.append((name, blocks.get(getattr(ws, "value", ws), "not made by the call")))
             return 0
         return call
@@ -43,9 +43,11 @@ def made(monkeypatch):
     keep = []
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch, "empty", recorded)
-    for name, at in (("mxfp8_bias_act_bwd", 10), ("nvfp4_moe_gemv", 14)):
+    for name, at in (("mxfp8_bias_act_bwd", 10), ("nvfp4_moe_gemv", 14), ("nvfp4_quantize", 0), ("nvfp4_gemm_quant", 6),
+                     ("grouped_nvfp4_gemm_quant", 11)):
         monkeypatch.setattr(bbs.lib, name, entry(name, at))
     monkeypatch.setattr(bbs, "_on_current", lambda stream, *t: 0)
+    monkeypatch.setattr(bbs, "_stream", lambda stream: 0)
     monkeypatch.setattr(bbs, "_used_on", lambda ws, stream: None)
     return seen
 
@@ -60,7 +62,25 @@ def moe(stream=None, ws=None):
                        bf(T, N), 1, ws=ws, stream=stream)
 
 
-CALLS = {"mxfp8_bias_act_bwd": bwd, "nvfp4_moe_gemv": moe}
+def nv(rows, cols):
+    return bbs.NVFP4Tensor.empty(rows, cols, device="cpu")
+
+
+def quantize(stream=None, ws=None):
+    bbs.nvfp4_quantize(bf(32, K), nv(32, K), amax_ws=ws, stream=stream)
+
+
+def gemm_quant(stream=None, ws=None):
+    bbs.nvfp4_gemm_quant(nv(32, K), nv(N, K), torch.ones(1), nv(32, N), gelu=True, ws=ws, stream=stream)
+
+
+def grouped_quant(stream=None, ws=None):
+    bbs.grouped_nvfp4_gemm_quant(nv(32, K), None, torch.zeros(2, dtype=torch.int32), 1, 32, nv(N, K), N, torch.ones(1),
+                                 nv(32, N), gelu=True, ws=ws, stream=stream)
+
+
+CALLS = {"mxfp8_bias_act_bwd": bwd, "nvfp4_moe_gemv": moe, "nvfp4_quantize": quantize, "nvfp4_gemm_quant": gemm_quant,
+         "grouped_nvfp4_gemm_quant": grouped_quant}
 
 
 @pytest.mark.parametrize("name", CALLS)
@@ -70,8 +90,8 @@ def test_own_workspace_is_made_on_the_calls_stream(made, name):
     assert made == [(name, "given"), (name, None)]
 
 
-@pytest.mark.parametrize("name,ws", [("mxfp8_bias_act_bwd", lambda: torch.zeros(bbs.BIAS_PARTS * N)),
-                                     ("nvfp4_moe_gemv", lambda: torch.zeros(1 << 16, dtype=torch.uint8))])
-def test_given_workspace_is_used(made, name, ws):
-    CALLS[name](stream="given", ws=ws())
+@pytest.mark.parametrize("name", CALLS)
+def test_given_workspace_is_used(made, name):
+    kind = torch.uint8 if name == "nvfp4_moe_gemv" else torch.float32
+    CALLS[name](stream="given", ws=torch.zeros(1 << 16, dtype=kind))
     assert made == [(name, "not made by the call")]
