@@ -932,8 +932,9 @@ int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t l
     int st;
     if (!any_act_ok(act)) return fail(BBS_EINVAL, "bad act");
     if (rows <= 0 || cols <= 0 || cols % 16) return fail(BBS_EINVAL, "rows and cols must be positive, cols %% 16 == 0");
-    // rows of a launch's ranges, columns of its grid
-    if (rows >= (int64_t)1 << 31 || cols >= (int64_t)1 << 31) return fail(BBS_ENOTSUP, "2^31 rows or columns or more");
+    // rows of a launch's ranges; columns of its grid, 256 threads for each 128: fewer than 2^32
+    if (rows >= (int64_t)1 << 31 || cols > ((int64_t)1 << 31) - 128)
+        return fail(BBS_ENOTSUP, "2^31 rows or more, or more than 2^31 - 128 columns");
     if ((st = check_rows_out(dY, BBS_OUT_BF16, cols, ldy, "dY"))) return st;
     if (dZ && (st = check_rows_out(dZ, BBS_OUT_BF16, cols, ldz, "dZ"))) return st;
     if (!dZ && !dbias) return fail(BBS_EINVAL, "neither dZ nor dbias");

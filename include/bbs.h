@@ -434,7 +434,8 @@ int nvfp4_gemm_bias_act(const bbs_fp4 *A, const bbs_fp4 *B, const void *bias, in
  * 8.  ws (with dbias): BBS_BIAS_PARTS * cols floats of device workspace, not
  * kept; calls that overlap in time need one each.  The order of the sums depends
  * on the sizes and the device's number of CUs alone.
- * Errors: BBS_EINVAL; BBS_ENOTSUP for 2^31 rows or columns or more. */
+ * Errors: BBS_EINVAL; BBS_ENOTSUP for 2^31 rows or more, or for more than
+ * 2^31 - 128 columns. */
 int mxfp8_bias_act_bwd(const uint16_t *dY, int64_t rows, int64_t cols, int64_t ldy, const bbs_mx8 *z8,
                        int32_t act, uint16_t *dZ, int64_t ldz, void *dbias, int32_t dbias_dtype,
                        float *ws, void *stream);
