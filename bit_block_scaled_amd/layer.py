@@ -489,6 +489,9 @@ class QGatedMLPInference:
         return y.reshape(*lead, N)
 
 
+_MORE_THAN_32_BITS = (torch.int64, torch.uint32, torch.uint64)
+
+
 class QMoEInference:
     """A mixture-of-experts layer from NVFP4 weights that are quantized when the
     object is made, each expert's as a tensor of its own: w_up [E, F, K], w_down [E, N,
@@ -524,9 +527,11 @@ class QMoEInference:
         _on_current(None, x, ids, self.up.codes, *(t for t in (weights, residual) if t is not None))
         x2 = _aligned(x.reshape(-1, K).to(torch.bfloat16).contiguous())
         T, k = x2.shape[0], ids.shape[-1]
-        # what does not fit 32 bits is no expert's number
         ids = ids.reshape(T, k)
-        ids = torch.where((ids >= 0) & (ids < self.experts), ids, -1).to(torch.int32).contiguous()
+        if ids.dtype in _MORE_THAN_32_BITS:              # what does not fit 32 bits is no expert's number
+            ids = ids.to(torch.int64)
+            ids = torch.where((ids >= 0) & (ids < self.experts), ids, -1)
+        ids = ids.to(torch.int32).contiguous()           # (the kernels drop what is outside [0, E))
         w = None if weights is None else weights.reshape(T, k).float().contiguous()
         r = _residual(residual, T, N)
         y = torch.empty((T, N), dtype=torch.bfloat16, device=x.device)

@@ -303,3 +303,16 @@ def test_inputs_at_any_address(L):
     e = L.QMoEInference(*W)
     v, ids = normal((70, 96), torch.bfloat16, 9), torch.arange(140, device=dev()).reshape(70, 2) % 4
     assert torch.equal(e(v, ids), e(moved(v), ids))
+
+
+def test_moe_inference_ids_of_every_type(L):
+    """More experts than a narrow type counts: the same answer from ids of every integer type."""
+    announce("QMoEInference: types of the ids")
+    E, k, F, K, N, T = 200, 3, 32, 48, 64, 6
+    f = L.QMoEInference(*(normal((E, a, b), torch.bfloat16, s, b ** -0.5) for s, a, b in ((1, F, K), (2, F, K), (3, N, F))))
+    x = normal((T, K), torch.bfloat16, 4)
+    ids = torch.randint(0, 128, (T, k), generator=torch.Generator().manual_seed(5)).to(dev())
+    want = f(x, ids)
+    assert bool((want.abs().amax(1) > 0).all())
+    for kind in (torch.int8, torch.uint8, torch.int16, torch.uint16, torch.int32, torch.uint32, torch.uint64):
+        assert torch.equal(f(x, ids.to(kind)), want), kind
