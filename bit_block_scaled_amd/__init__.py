@@ -513,9 +513,17 @@ def _vector(t, n, name):
 
 
 def _mx8_shape(t, rows, cols, name):
-    """An MXFP8Tensor's sizes, against its own tensors."""
+    """An MXFP8Tensor's sizes, and that its tensors hold as much."""
     if not isinstance(t, MXFP8Tensor) or (t.rows, t.cols) != (rows, cols):
         raise ValueError(f"{name} must be an MXFP8Tensor of {rows} x {cols}")
+    for v, n in ((t.codes, rows * cols), (t.scales, rows * (cols // 32))):
+        if v.element_size() != 1 or v.numel() < n or not v.is_contiguous():
+            raise ValueError(f"{name} must hold {rows} x {cols} adjacent codes and their scales")
+
+
+def _parts(q):
+    """The tensors of an operand."""
+    return (q.codes, q.scales, q.s_dec) if isinstance(q, NVFP4Tensor) else (q.codes, q.scales)
 
 
 def nvfp4_gemm_bias_act(A, B, out, out_dtype, bias=None, act=ACT_NONE, residual=None, z_ckpt=None, ldo=None,
@@ -532,7 +540,7 @@ def nvfp4_gemm_bias_act(A, B, out, out_dtype, bias=None, act=ACT_NONE, residual=
     if z_ckpt is not None:
         _mx8_shape(z_ckpt, M, N, "z_ckpt")
     more = [t for t in (bias, residual) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
-    s = _on_current(stream, A.codes, B.codes, out, *more)
+    s = _on_current(stream, *_parts(A), *_parts(B), out, *more)
     ad, bd = A.desc(), B.desc()
     zd = z_ckpt.desc() if z_ckpt is not None else None
     _check(lib.nvfp4_gemm_bias_act(C.byref(ad), C.byref(bd), b, b_dtype, act, _ptr(residual), ldr or 0,
@@ -577,7 +585,9 @@ def nvfp4_gemv_bias_act(fmt, x, W, y, y_dtype, bias=None, act=ACT_NONE, residual
     b, b_dtype = _vector(bias, W.rows, "bias")
     if residual is not None:
         ldr = _output_ld(residual, y_dtype, T, W.rows, ldr, "residual")
-    if any(t is not None and t.get_device() != x.get_device() for t in (bias, residual)):
+    dev = x.get_device()
+    if (bias is not None and bias.get_device() != dev) or (residual is not None and residual.get_device() != dev) or \
+            W.scales.get_device() != dev or (fmt == FMT_NVFP4 and W.s_dec.get_device() != dev):
         raise ValueError("the tensors must be on one GPU")
     status = lib.nvfp4_gemv_bias_act(fmt, x.data_ptr(), T, ldx, W.packed(), b, b_dtype, act, _ptr(residual), ldr or 0,
                                      y.data_ptr(), y_dtype, ldy, s)
@@ -613,9 +623,10 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
     for w in (Wu, Wd) if Wg is None else (Wu, Wd, Wg):
         if kind is None or not isinstance(w, kind):
             raise ValueError("fmt must be FMT_NVFP4 or FMT_MXFP4, and the weights in that format")
-        if kind is NVFP4Tensor and w.s_dec.numel() != experts:
-            raise ValueError("NVFP4 weights need one decode scale an expert")
-        tensors.append(w.codes)
+        if kind is NVFP4Tensor and (w.s_dec.numel() != experts or w.s_dec.dtype != torch.float32 or
+                                    not w.s_dec.is_contiguous()):
+            raise ValueError("NVFP4 weights need one float32 decode scale an expert, adjacent")
+        tensors.extend(_parts(w))
     if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous int32 tensor of {T} rows")
     k = ids.shape[1]
