@@ -63,9 +63,9 @@ class QuantArgs(C.Structure):
                 ("gelu", C.c_int32)]
 
 
-# Fp4Desc and Mx4Desc as bytes
+# Fp4Desc, and Mx8Desc or Mx4Desc, as bytes
 _FP4_PACK = struct.Struct("@PPPqqii").pack
-_MX4_PACK = struct.Struct("@PPqq").pack
+_MX_PACK = struct.Struct("@PPqq").pack
 
 
 class BbsError(RuntimeError):
@@ -105,9 +105,8 @@ def _load():
                                          C.POINTER(Mx8Desc), i32, vp, vp, i32, i64, vp]
     lib.nvfp4_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i64, vp]
     lib.nvfp4_gated_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, vp, i32, i64, vp]
-    lib.nvfp4_gemm_bias_act.argtypes = [C.POINTER(Fp4Desc), C.POINTER(Fp4Desc), vp, i32, i32, vp, i64,
-                                        C.POINTER(Mx8Desc), vp, i32, i64, vp]
-    lib.mxfp8_bias_act_bwd.argtypes = [vp, i64, i64, i64, C.POINTER(Mx8Desc), i32, vp, i64, vp, i32, vp, vp]
+    lib.nvfp4_gemm_bias_act.argtypes = [vp, vp, vp, i32, i32, vp, i64, vp, vp, i32, i64, vp]
+    lib.mxfp8_bias_act_bwd.argtypes = [vp, i64, i64, i64, vp, i32, vp, i64, vp, i32, vp, vp]
     lib.nvfp4_gemv_bias_act.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, i64, vp, i32, i64, vp]
     lib.nvfp4_moe_gemv.argtypes = [i32, vp, i64, i64, vp, vp, i32, i32, vp, vp, vp, i32, vp, i64, vp, vp, i32, i64, vp]
     lib.nvfp4_moe_ws_bytes.argtypes = [i64, i32, i32, i64, i64]
@@ -195,6 +194,10 @@ class MXFP8Tensor:
     def desc(self):
         return Mx8Desc(_ptr(self.codes), _ptr(self.scales), self.rows, self.cols)
 
+    def packed(self):
+        """As NVFP4Tensor.packed."""
+        return _MX_PACK(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+
 
 class MXFP4Tensor:
     """codes [rows, cols/2] u8 (E2M1 pairs, even column low), scales [rows, cols/32] u8 (E8M0)."""
@@ -213,7 +216,7 @@ class MXFP4Tensor:
 
     def packed(self):
         """As NVFP4Tensor.packed."""
-        return _MX4_PACK(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
+        return _MX_PACK(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
 
 
 class S2F6Tensor:
@@ -516,14 +519,10 @@ def _mx8_shape(t, rows, cols, name):
     """An MXFP8Tensor's sizes, and that its tensors hold as much."""
     if not isinstance(t, MXFP8Tensor) or (t.rows, t.cols) != (rows, cols):
         raise ValueError(f"{name} must be an MXFP8Tensor of {rows} x {cols}")
-    for v, n in ((t.codes, rows * cols), (t.scales, rows * (cols // 32))):
-        if v.element_size() != 1 or v.numel() < n or not v.is_contiguous():
-            raise ValueError(f"{name} must hold {rows} x {cols} adjacent codes and their scales")
-
-
-def _parts(q):
-    """The tensors of an operand."""
-    return (q.codes, q.scales, q.s_dec) if isinstance(q, NVFP4Tensor) else (q.codes, q.scales)
+    c, s = t.codes, t.scales
+    if c.itemsize != 1 or s.itemsize != 1 or c.numel() < rows * cols or s.numel() < rows * (cols // 32) or \
+            not (c.is_contiguous() and s.is_contiguous()):
+        raise ValueError(f"{name} must hold {rows} x {cols} adjacent codes and their scales")
 
 
 def nvfp4_gemm_bias_act(A, B, out, out_dtype, bias=None, act=ACT_NONE, residual=None, z_ckpt=None, ldo=None,
@@ -537,14 +536,18 @@ def nvfp4_gemm_bias_act(A, B, out, out_dtype, bias=None, act=ACT_NONE, residual=
     if residual is not None:
         ldr = _output_ld(residual, out_dtype, M, N, ldr, "residual")
     b, b_dtype = _vector(bias, N, "bias")
+    tensors, zd = [out, A.codes, A.scales, A.s_dec, B.codes, B.scales, B.s_dec], None
+    if bias is not None:
+        tensors.append(bias)
+    if residual is not None:
+        tensors.append(residual)
     if z_ckpt is not None:
         _mx8_shape(z_ckpt, M, N, "z_ckpt")
-    more = [t for t in (bias, residual) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
-    s = _on_current(stream, *_parts(A), *_parts(B), out, *more)
-    ad, bd = A.desc(), B.desc()
-    zd = z_ckpt.desc() if z_ckpt is not None else None
-    _check(lib.nvfp4_gemm_bias_act(C.byref(ad), C.byref(bd), b, b_dtype, act, _ptr(residual), ldr or 0,
-                                   C.byref(zd) if zd is not None else None, _ptr(out), out_dtype, ldo, s))
+        tensors += (z_ckpt.codes, z_ckpt.scales)
+        zd = z_ckpt.packed()
+    s = _on_current(stream, *tensors)
+    _check(lib.nvfp4_gemm_bias_act(A.packed(), B.packed(), b, b_dtype, act, _ptr(residual), ldr or 0, zd, _ptr(out),
+                                   out_dtype, ldo, s))
 
 
 def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=None):
@@ -567,11 +570,16 @@ def mxfp8_bias_act_bwd(dY, z_ckpt, act, dZ=None, dbias=None, ws=None, stream=Non
             ws = _workspace(lambda: torch.empty((BIAS_PARTS * N,), dtype=torch.float32, device=dY.device), stream)
         elif ws.dtype != torch.float32 or not ws.is_contiguous() or ws.numel() < BIAS_PARTS * N:
             raise ValueError(f"ws must hold {BIAS_PARTS * N} adjacent float32 values")
-    more = [t for t in (dZ, dbias, ws) if t is not None] + ([z_ckpt.codes, z_ckpt.scales] if z_ckpt is not None else [])
-    s = _on_current(stream, dY, *more)
-    zd = z_ckpt.desc() if z_ckpt is not None else None
-    _check(lib.mxfp8_bias_act_bwd(_ptr(dY), M, N, ldy, C.byref(zd) if zd is not None else None, act, _ptr(dZ), ldz,
-                                  b, b_dtype, _ptr(ws), s))
+    tensors, zd = [dY], None
+    if z_ckpt is not None:
+        tensors += (z_ckpt.codes, z_ckpt.scales)
+        zd = z_ckpt.packed()
+    if dZ is not None:
+        tensors.append(dZ)
+    if dbias is not None:
+        tensors += (dbias, ws)
+    s = _on_current(stream, *tensors)
+    _check(lib.mxfp8_bias_act_bwd(_ptr(dY), M, N, ldy, zd, act, _ptr(dZ), ldz, b, b_dtype, _ptr(ws), s))
     if own:
         _used_on(ws, stream)
 
@@ -623,10 +631,13 @@ def nvfp4_moe_gemv(fmt, x, ids, weights, experts, Wg, Wu, Wd, y, y_dtype, act=AC
     for w in (Wu, Wd) if Wg is None else (Wu, Wd, Wg):
         if kind is None or not isinstance(w, kind):
             raise ValueError("fmt must be FMT_NVFP4 or FMT_MXFP4, and the weights in that format")
-        if kind is NVFP4Tensor and (w.s_dec.numel() != experts or w.s_dec.dtype != torch.float32 or
-                                    not w.s_dec.is_contiguous()):
-            raise ValueError("NVFP4 weights need one float32 decode scale an expert, adjacent")
-        tensors.extend(_parts(w))
+        if kind is NVFP4Tensor:
+            d = w.s_dec
+            if d.numel() != experts or d.dtype is not torch.float32 or not d.is_contiguous():
+                raise ValueError("NVFP4 weights need one float32 decode scale an expert, adjacent")
+            tensors += (w.codes, w.scales, d)
+        else:
+            tensors += (w.codes, w.scales)
     if ids.dim() != 2 or ids.shape[0] != T or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError(f"ids must be a contiguous int32 tensor of {T} rows")
     k = ids.shape[1]
