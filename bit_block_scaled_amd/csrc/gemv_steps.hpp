@@ -158,7 +158,8 @@ __device__ __forceinline__ s16x4 codes4(uint32_t w, int h) {
                                                 __builtin_bit_cast(uint32_t, b)));
 }
 
-// TT tokens are computed (1, 2 or 4), those from p.T on are not stored.
+// TT <= 4 rows of the products are summed: tokens, or the parts of tokens' hidden values.
+// What stands in a row that the caller does not need stays in that row's sum.
 template <int SC, int NM, int TT, int R>
 __device__ __forceinline__ void add_step(float (&acc)[NM][R][TT], const Step<NM, R> &st) {
 #pragma unroll

@@ -40,23 +40,6 @@ hipError_t launch_linear(const LinearParams &p, bool bf16_out, hipStream_t s);
 hipError_t launch_linear_big(const LinearParams &p, bool bf16_out, hipStream_t s);
 hipError_t launch_bias_act_bwd(const BiasActBwdParams &p, hipStream_t s);
 
-// bias[n .. n + 3] in FP32 (n a multiple of 4, n < N).
-__device__ __forceinline__ void load_bias4(const void *bias, int bf16, int64_t n, float (&b)[4]) {
-    if (bf16) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(bias) + n);
-        b[0] = __uint_as_float(v.x << 16);
-        b[1] = __uint_as_float(v.x & 0xFFFF0000u);
-        b[2] = __uint_as_float(v.y << 16);
-        b[3] = __uint_as_float(v.y & 0xFFFF0000u);
-    } else {
-        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(bias) + n);
-        b[0] = v.x;
-        b[1] = v.y;
-        b[2] = v.z;
-        b[3] = v.w;
-    }
-}
-
 // act is the same for every lane, so it is chosen once for NV values.
 template <bool TO_BF16, int NV, typename V>
 __device__ __forceinline__ void act_all(V &v, int act) {

@@ -422,3 +422,29 @@ def test_own_workspace_on_another_stream(bbs, monkeypatch):
     assert other.data_ptr() != made[0][0]
     torch.cuda.synchronize()
     assert busy and torch.equal(db, want)
+
+
+def test_bwd_over_a_grid_against_differences(bbs):
+    """As test_bwd_is_the_gradient_of_the_forward_pass, at every value of four significant
+    bits from 2^-4 to 7.5, which the checkpoint holds exactly beside any other of them."""
+    announce("linear bwd against differences, grid")
+    e, m = torch.arange(-7, -1, device=dev()), torch.arange(8, 16, device=dev())
+    b = torch.ldexp(m[None, :].float(), e[:, None]).flatten()
+    b = torch.cat([b, -b])
+    M, N, K, h = 16, b.numel(), 16, 2.0 ** -6
+    A, W = random_nv(bbs, M, K, False, 1), random_nv(bbs, N, K, False, 2)
+    A.codes.zero_()                                                     # z is the bias
+    dy = normal((M, N), torch.bfloat16, 3)
+    for act in ("silu", "gelu"):
+        z8 = bbs.MXFP8Tensor.empty(M, N, device=dev())
+        y = [torch.empty((M, N), device=dev()) for _ in range(3)]
+        for t, d in zip(y, (-h, h, 0.0)):
+            bbs.nvfp4_gemm_bias_act(A, W, t, 0, bias=b + d, act=ACTS[act], z_ckpt=z8)
+        assert torch.equal(mx64(z8), b.double().expand(M, N))
+        dz, db = torch.empty((M, N), dtype=torch.bfloat16, device=dev()), torch.empty((N,), device=dev())
+        bbs.mxfp8_bias_act_bwd(dy, z8, ACTS[act], dz, db)
+        diff = (y[1].double() - y[0].double()) / (2 * h) * dy.double()
+        # h^2 / 6 of the third derivative (below 8) and the rounding of two values
+        off = dy.double().abs() * (8 * h * h / 6 + 32 * ULP * (1 + b.double().abs()) / h)
+        assert bool(((dz.double() - diff).abs() <= off + (diff.abs() + off) * 2.0 ** -8).all())
+        assert bool(((db.double() - diff.sum(0)).abs() <= off.sum(0) + 64 * ULP * dy.double().abs().sum(0)).all())
