@@ -12,9 +12,10 @@
 //
 // Bound by the products' matrix instructions, and beside them by the epilogue's
 // vector ones (22 a value with GELU and a checkpoint), during which a SIMD's only
-// wave leaves its matrix unit idle.  Measured, BF16 outputs: 8192 x 4096 x 14336
-// with bias and residual 691 us (1.39 PFLOP/s), the product alone 683; 8192 x 14336 x
-// 4096 alone 694 us, with bias 702, with bias, GELU and checkpoint 754 (1.28).
+// wave leaves its matrix unit idle.  Measured, BF16 outputs, replayed from a graph on one
+// card (others were up to 5% slower in all of them): 8192 x 4096 x 14336 with bias and
+// residual 659 us (1.46 PFLOP/s), the product alone 650; 8192 x 14336 x 4096 alone 663
+// us, with bias 673, with bias, GELU and checkpoint 727 (1.32).
 #include "gemm_nvfp4_tiles.hpp"
 #include "linear.hpp"
 

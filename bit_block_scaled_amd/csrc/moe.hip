@@ -1024,9 +1024,13 @@ bool streams(const MoeParams &p) {
 // every four of an expert.  NVFP4, up to eight tokens, against the other two forms: 8 of
 // 64 experts, 5 tokens 71.5 us and 85.9, 8 tokens 94.7 and 102; 2 of 8, 6 tokens 130 and
 // 142, 8 tokens 154 and 152; 2 of 16 small ones, 8 tokens 15.3 and 17.2 (16 tokens and 8 of 64:
-// 198 and 135).  MXFP4 streams sooner, as its codes are cheap to expand: 2 of 8, 3 tokens
-// 103 and 85.8, 4 tokens 138 and 119; but below the streaming kernels' size 4 tokens 25.0 and
-// 30.3, 5 tokens 20.7 and 17.5.
+// 198 and 135).  That is with BF16 outputs; for FP32 ones the down projection takes one
+// token at a time and expands its codes again for each: 8 of 64, 3 tokens 49.9 and 72.3, 5
+// tokens 74.9 and 86.5, 8 tokens 102 and 104; 2 of 8, 3 tokens 90.6 and 93.8, but 6 tokens
+// 151 and 143, 8 tokens 185 and 155: from about two tokens an expert on the bound of eight
+// tokens is too high there.  MXFP4 streams sooner, as its codes are cheap to expand: 2 of 8,
+// 3 tokens 103 and 85.8, 4 tokens 138 and 119; but below the streaming kernels' size 4 tokens
+// 25.0 and 30.3, 5 tokens 20.7 and 17.5.
 template <int SC>
 bool few_tokens(const MoeParams &p) {
     if (SC != kRows32) return p.T <= 8;

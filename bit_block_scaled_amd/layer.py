@@ -25,7 +25,9 @@ With bias, act or a residual, Y = act(X W^T + b) + R is one kernel that keeps
 z = X W^T + b as an 8-bit (MXFP8) checkpoint; the backward pass first takes dY
 through the activation and sums the bias' gradient in one pass, and goes on from
 dZ as above.  Kept then, in bits a value: 4.5 for X, 8.25 for z with an
-activation, and of those only what the wanted gradients read.
+activation, and of those only what the wanted gradients read.  Outputs are BF16, and so
+is a residual: one of another type is rounded to BF16 first, then added in FP32 and
+rounded with the sum.
 QLinearInference holds the quantized weight of such a layer, and
 QMoEInference a layer of experts; up to GEMV_MAX_TOKENS tokens are answered by the
 few-token kernels (activations in BF16).
@@ -235,7 +237,8 @@ class QLinear(torch.nn.Module):
     """Linear layer whose forward and backward GEMMs run in NVFP4 / MXFP8 as above.
     weight: [out_features, in_features], BF16; bias: [out_features] or None; act:
     None, "silu" or "gelu", applied to the product and the bias.  The call takes a
-    residual [..., out_features] that is added at the end."""
+    residual [..., out_features] that is added at the end, in FP32 but as its BF16 values
+    (an FP32 residual loses what BF16 does not hold)."""
 
     def __init__(self, in_features, out_features, seed=0, rht_signs=0x5A3C, device="cuda",
                  dtype=torch.bfloat16, bias=False, act=None):
@@ -280,7 +283,8 @@ class QLinearInference:
     object is made (a later change of the given tensors does not reach it).  Up to
     GEMV_MAX_TOKENS tokens the activations stay BF16; more tokens are quantized to
     NVFP4 (padded to a multiple of 16 rows) with one decode scale for the call, so
-    a token's answer then also depends on the other tokens."""
+    a token's answer then also depends on the other tokens.  Bias and residual are
+    added in FP32; a residual of another type than BF16 is rounded to BF16 first."""
 
     def __init__(self, weight, bias=None, act=None):
         if act is not None and act not in _ACTS:
@@ -498,7 +502,7 @@ class QMoEInference:
     F], and w_gate [E, F, K] for gated experts (None: plain ones, act may then be
     None).  The call takes the router's choice: ids [..., k] (integers; outside
     [0, E): no expert) and weights [..., k] (None: 1), and an optional residual
-    [..., N].  GEMV_MAX_TOKENS tokens go through the kernels at a time (many more
+    [..., N], added in FP32 as its BF16 values.  GEMV_MAX_TOKENS tokens go through the kernels at a time (many more
     tokens read the experts' weights again for each group of them)."""
 
     def __init__(self, w_gate, w_up, w_down, act="silu"):
