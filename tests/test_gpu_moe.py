@@ -386,3 +386,41 @@ def test_own_workspace_leaves_pending_work_alone(bbs, monkeypatch, op):
     assert torch.equal(got, want)
     torch.cuda.synchronize()
     assert bool((sums == 7 * 256).all())
+
+
+def test_own_workspaces_in_a_capture_of_two_streams(bbs):
+    """Calls on a given stream that a capture forks to, each with a workspace of its own, and
+    others beside them on the capturing stream: every replay gives the eager bits."""
+    announce("own workspaces, captured on a forked stream")
+    q = problem(bbs, 20, 1)
+    dy, x = normal((512, 256), torch.bfloat16, 1), normal((64, 256), torch.bfloat16, 2)
+    s = torch.cuda.Stream()
+
+    def both(stream):
+        out = []
+        for on in (stream, None):
+            y, db = torch.empty_like(q["r"]), torch.empty((256,), device=dev())
+            row, col = bbs.NVFP4Tensor.empty(64, 256, device=dev()), bbs.NVFP4Tensor.empty(256, 64, device=dev())
+            out += [y, db, row.codes, row.scales, row.s_dec, col.codes, col.scales, col.s_dec]
+            if on is not None:
+                on.wait_stream(torch.cuda.current_stream())
+            bbs.nvfp4_moe_gemv(0, q["x"], q["ids"], q["w"], 16, *q["W"], y, 1, residual=q["r"], stream=on)
+            bbs.mxfp8_bias_act_bwd(dy, None, bbs.ACT_NONE, None, db, stream=on)
+            bbs.nvfp4_quantize(x, row, col, stream=on)
+        torch.cuda.current_stream().wait_stream(s)
+        return out
+
+    want = both(None)
+    for a, b in zip(want, both(s)):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = both(s)
+    for i in range(4):
+        q["x"].copy_(torch.roll(q["x"], 1, 1))
+        dy.copy_(torch.roll(dy, 1, 0)), x.copy_(torch.roll(x, 1, 1))
+        graph.replay()
+        eager = both(s)
+        torch.cuda.synchronize()
+        assert same(eager, cap), i
